@@ -16,8 +16,9 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe_route.so")
 
 SOURCES = ["api.cpp", "geometry.cpp", "route.hip", "scatter.hip", "combine.hip", "route_fused.hip",
-           "scratch.hip"]
-HEADERS = ["device_common.hpp", "internal.hpp", "route_device.hpp", "rows_device.hpp"]
+           "scratch.hip", "api_train.cpp", "gate.hip", "grad.hip", "embedding.hip"]
+HEADERS = ["api_common.hpp", "device_common.hpp", "internal.hpp", "route_device.hpp",
+           "rows_device.hpp", "train.hpp", "train_device.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -10,16 +10,16 @@
 #include <string>
 
 #include "moe_route.h"
+#include "api_common.hpp"
 #include "internal.hpp"
-
-#define MOE_API extern "C" __attribute__((visibility("default")))
 
 namespace {
 
 thread_local std::string g_last_error;
 
-constexpr int kTile = 1024;  // entries per routing tile (matches the rank kernel)
-constexpr int64_t kMaxRows = INT32_MAX;
+}  // namespace
+
+namespace moe {
 
 int fail(int status, const char* fmt, ...) {
     char buf[512];
@@ -31,30 +31,52 @@ int fail(int status, const char* fmt, ...) {
     return status;
 }
 
-int ok() { return MOE_OK; }
-
-int hip_fail(hipError_t e, const char* where) {
-    return fail(MOE_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
+int check_ws(void* ws, size_t ws_bytes, size_t need) {
+    if (ws_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed",
+                    ws_bytes, need);
+    if (need > 0 && !ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if (ws && !aligned(ws, 256)) return fail(MOE_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    return MOE_OK;
 }
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+int check_rows_ptr(const void* p, int64_t rows, const char* name) {
+    if (rows > 0 && !p) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
+    if (p && !aligned(p, 16)) return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+    return MOE_OK;
+}
 
-size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+int check_H(int64_t H, bool quantized_rows) {
+    if (H <= 0 || H % 8 != 0)
+        return fail(MOE_ERR_INVALID_ARG, "H=%lld must be a positive multiple of 8", (long long)H);
+    if (quantized_rows && H % 128 != 0)
+        return fail(MOE_ERR_INVALID_ARG, "H=%lld must be a multiple of 128 for fp8",
+                    (long long)H);
+    if (H > ((int64_t)1 << 24))
+        return fail(MOE_ERR_INVALID_ARG, "H=%lld exceeds 2^24", (long long)H);
+    return MOE_OK;
+}
+
+}  // namespace moe
+
+namespace {
+
+using moe::aligned;
+using moe::Carve;
+using moe::check_H;
+using moe::check_rows_ptr;
+using moe::check_ws;
+using moe::fail;
+using moe::kMaxRows;
+using moe::quantized;
+
+constexpr int kTile = 1024;  // entries per routing tile (matches the rank kernel)
+
+int ok() { return MOE_OK; }
 
 int elem_bytes(moe_dtype d) { return d == MOE_F32 ? 4 : (d == MOE_BF16 ? 2 : 1); }
 
-bool quantized(moe_dtype d) { return d == MOE_FP8_E4M3 || d == MOE_FP4_E2M1; }
-
-// Workspace carving.  Sizes depend only on (T, K, E, R).
-struct Carve {
-    size_t total = 0;
-    size_t take(size_t bytes) {
-        const size_t at = total;
-        total += align256(bytes);
-        return at;
-    }
-};
-
+// Workspace sizes depend only on (T, K, E, R).
 struct RouteWs {  // one routing level: N entries over NK keys
     size_t local_rank, tile_cnt, tile_flags, off;
     int64_t tiles;
@@ -101,44 +123,6 @@ int check_routing(int64_t T, int K, int E, const int32_t* idx) {
     if (idx && !aligned(idx, 4)) return fail(MOE_ERR_INVALID_ARG, "idx is not 4-byte aligned");
     return MOE_OK;
 }
-
-int check_ws(void* ws, size_t ws_bytes, size_t need) {
-    if (ws_bytes < need)
-        return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed",
-                    ws_bytes, need);
-    if (need > 0 && !ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
-    if (ws && !aligned(ws, 256)) return fail(MOE_ERR_WORKSPACE, "workspace is not 256-byte aligned");
-    return MOE_OK;
-}
-
-int check_rows_ptr(const void* p, int64_t rows, const char* name) {
-    if (rows > 0 && !p) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
-    if (p && !aligned(p, 16)) return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
-    return MOE_OK;
-}
-
-int check_H(int64_t H, bool fp8) {
-    if (H <= 0 || H % 8 != 0)
-        return fail(MOE_ERR_INVALID_ARG, "H=%lld must be a positive multiple of 8", (long long)H);
-    if (fp8 && H % 128 != 0)
-        return fail(MOE_ERR_INVALID_ARG, "H=%lld must be a multiple of 128 for fp8",
-                    (long long)H);
-    if (H > ((int64_t)1 << 24))
-        return fail(MOE_ERR_INVALID_ARG, "H=%lld exceeds 2^24", (long long)H);
-    return MOE_OK;
-}
-
-#define MOE_TRY(expr)                 \
-    do {                              \
-        const int st_ = (expr);       \
-        if (st_ != MOE_OK) return st_; \
-    } while (0)
-
-#define MOE_HIP(expr, where)                  \
-    do {                                      \
-        const hipError_t e_ = (expr);         \
-        if (e_ != hipSuccess) return hip_fail(e_, where); \
-    } while (0)
 
 // Rank pass + scan pass for one routing level.
 struct LevelOut {
@@ -223,7 +207,7 @@ moe::SlotArgs slot_args(void* ws, const RouteWs& L, const int32_t* idx, int K, i
 
 }  // namespace
 
-MOE_API int moe_version(void) { return (1 << 16) | 2; }
+MOE_API int moe_version(void) { return (1 << 16) | 3; }
 
 MOE_API const char* moe_geometry(void) { return moe::geometry_text(); }
 

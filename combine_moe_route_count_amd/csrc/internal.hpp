@@ -16,6 +16,18 @@ enum class KeyKind {
     Experts,    // f = t*K + k, key = idx[f] when valid
     Ranks,      // f = t*R + r, key = r when r is in token t's rank mask
     Survivors,  // f = t*K + k, key = idx[f] when valid and its recv row exists
+    Digits,     // key = one digit of token id f (one-launch routing only)
+};
+
+// Token ids and the digit of them that is the key.  First pass (total null): raw
+// ids of id_bytes, valid in [0,V).  Later passes: int32 ids that the earlier pass
+// moved, the first *total entries.
+struct DigitSource {
+    const void* ids;
+    int id_bytes;
+    int64_t V;
+    const int32_t* total;
+    int shift, mask;
 };
 
 struct RankArgs {
@@ -134,6 +146,7 @@ struct RouteFusedArgs {
     KeyKind kind;
     const int32_t* idx;
     const int32_t* rank_slot;  // Survivors only
+    DigitSource digits;        // Digits only
     int64_t N;          // entries
     int K, E, R;
     int nbits;          // key bits of NK

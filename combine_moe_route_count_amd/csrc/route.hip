@@ -68,6 +68,8 @@ hipError_t launch_rank(const RankArgs& a, hipStream_t s) {
                 SurvivorKeys{a.idx, a.rank_slot, a.K, a.E, a.R, a.E / a.R}, a.N, a.NK, nbits,
                 a.local_rank, a.tile_cnt, a.tile_flags);
             break;
+        case KeyKind::Digits:   // digits have at most kFusedMaxKeys values: route_fused.hip
+            return hipErrorInvalidValue;
     }
     return hipGetLastError();
 }

@@ -49,6 +49,21 @@ struct SurvivorKeys {
     }
 };
 
+// f = position of a token id; the key is one digit of it.
+struct DigitKeys {
+    DigitSource d;
+    __device__ __forceinline__ int operator()(int64_t f) const {
+        if (d.total) {
+            if (f >= *d.total) return kKeySkip;
+            return (((const int32_t*)d.ids)[f] >> d.shift) & d.mask;
+        }
+        const int64_t id = d.id_bytes == 8 ? ((const int64_t*)d.ids)[f]
+                                           : (int64_t)((const int32_t*)d.ids)[f];
+        if (id < 0 || id >= d.V) return id == -1 ? kKeySkip : kKeyInvalid;
+        return (int)(id >> d.shift) & d.mask;
+    }
+};
+
 // Stable ranks of one tile of WAVES*CHUNKS*64 entries.  Each wave owns a
 // contiguous run of CHUNKS*64 entries and walks it in 64-entry chunks; equal
 // keys are found with one ballot per key bit, a lane's rank is the number of

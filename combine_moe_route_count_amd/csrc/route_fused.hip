@@ -126,6 +126,9 @@ hipError_t launch_route_fused(const RouteFusedArgs& a, hipStream_t s) {
             route_fused_kernel<<<grid, block, lds, s>>>(
                 SurvivorKeys{a.idx, a.rank_slot, a.K, a.E, a.R, a.E / a.R}, a);
             break;
+        case KeyKind::Digits:
+            route_fused_kernel<<<grid, block, lds, s>>>(DigitKeys{a.digits}, a);
+            break;
     }
     return hipGetLastError();
 }

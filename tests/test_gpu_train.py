@@ -77,13 +77,15 @@ def _gate_ref(l, idx, renorm, scale):
 
 
 def _gate_rel(l, K):
-    """Relative error of a weight: exp's argument l - top is rounded once (|l - top| * u absolute,
-    so relative in exp), exp itself is within 2 u, the sum has at most E terms each off by the same
-    (weighted by p, so at most the largest |l - top| that is not negligible), then a division and a
-    product.  exp(-104) underflows f32, and arguments past that only matter below TINY."""
+    """Relative error of a weight, in units of u.  exp(x), x = l - top <= 0, as 2^(x*log2 e): x and
+    the product are rounded once each and log2(e) is 0.2 u off, all of it in the exponent, so
+    2.2 |x|; the power itself 2.  The sum: terms weigh p_j = e^x_j / S with S >= 1, so their own
+    errors add sum p_j (2.2 |x_j| + 2) <= 2.2 E/e + 2 < 0.81 E + 2 (t e^-t <= 1/e), its additions at
+    most E.  Then a division and a product: 2.2 d + 1.81 E + 6 in all.  Arguments past 104
+    underflow f32 and only matter below TINY."""
     z = torch.where(torch.isfinite(l.double()), l.double(), 0.0)
     d = (z.amax(1, keepdim=True) - z.amin(1, keepdim=True)).clamp(max=104.0)
-    return (2 * d + l.shape[1] + 8) * U
+    return (2.25 * d + 2 * l.shape[1] + 8) * U
 
 
 def _logits(g, T, E, dt, kind):

@@ -11,7 +11,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._lib import (MOE_BF16, MOE_F32, MOE_FP4_E2M1, MOE_FP8_E4M3, _check, _stream, load, ptr)
+from ._lib import (MOE_BF16, MOE_F32, MOE_FP4_E2M1, MOE_FP8_E4M3, _check, _raw_stream, load, ptr)
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -58,34 +58,49 @@ def _need(cond: bool, msg: str) -> None:
         raise ValueError(msg)
 
 
-def _tensor(name: str, t: torch.Tensor, shape, dtypes, dev: torch.device) -> None:
-    """t is a contiguous tensor of this shape, one of these types, on dev."""
+# The checks run on every call, and the smallest calls take a few microseconds on
+# the GPU: one expression decides, and the reason is only looked for when it fails.
+# dev is a device index.
+def _tensor(name: str, t: torch.Tensor, shape, dtypes, dev: int) -> None:
+    """t is a contiguous tensor of this shape, one of these types, on GPU dev."""
+    if (t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev
+            and t.is_cuda):
+        return
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has type {t.dtype}, not one of {[str(d) for d in dtypes]}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} is not contiguous")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
 
 
-def _gpu(name: str, t: torch.Tensor, dim: int) -> torch.device:
+def _gpu(name: str, t: torch.Tensor, dim: int) -> int:
+    """The index of the GPU that t, of dim dimensions, is on."""
     if not t.is_cuda:
         raise ValueError(f"{name} is not on a GPU")
     if t.dim() != dim:
         raise ValueError(f"{name} has {t.dim()} dimensions, not {dim}")
-    return t.device
+    return t.get_device()
 
 
-def _call(name: str, dev: torch.device, *args) -> None:
-    """The library call on dev's current stream, with dev current."""
-    fn = getattr(_lib(), name)
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(dev)))
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _stream_of(dev: int):
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _call(name: str, dev: int, *args) -> None:
+    """The library call on GPU dev's current stream, with dev current."""
+    fn = getattr(_bound or _lib(), name)
+    if dev == _current_device():
+        status = fn(*args, _stream_of(dev))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(dev)))
+            status = fn(*args, _stream_of(dev))
+    if status:
+        _check(status)
 
 
 def gate(logits: torch.Tensor, K: int, renormalize: bool = True, scale: float = 1.0,
@@ -283,10 +298,10 @@ def embedding_backward(dout: torch.Tensor, ids: torch.Tensor, V: int, scale: flo
         dtable = torch.empty((V, H), dtype=dtable_dtype, device=dev)
     _tensor("dtable", dtable, (V, H), _FLOAT, dev)
     if ws is None:
-        ws = embedding_workspace(N, V, H, dev)
+        ws = embedding_workspace(N, V, H, torch.device("cuda", dev))
     else:
-        _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev,
-              f"ws must be contiguous uint8 on {dev}")
+        _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.is_cuda and ws.get_device() == dev,
+              f"ws must be contiguous uint8 on cuda:{dev}")
     _call("moe_embedding_backward", dev, ptr(dout), _FLOAT[dout.dtype], ptr(ids), _IDS[ids.dtype],
           N, V, H, scale, int(accumulate), ptr(dtable), _FLOAT[dtable.dtype], ptr(ws), ws.numel())
     return dtable

@@ -1,20 +1,23 @@
-// gate.hip - the top-k gate and its gradient: one wave per token.
+// gate.hip - the top-k gate and its gradient.
 //
-// Lane l holds the V consecutive logits [l*V, l*V + V) of its token, V the smallest
-// power of two with 64*V >= E, so the lowest lane that holds a value also holds its
-// lowest expert id.  Each lane sorts its logits once, as ordered integer keys, equal
-// ones by id.  A choice is then one wave maximum over the lanes' heads and a pop of
-// the list it came from; K choices need no memory.  The softmax follows in the same registers: with m the largest logit,
-// p_j = exp(l_j - m) / sum.
+// A token belongs to a group of G lanes: 64, or 16 (four tokens per wave) where its
+// logits still fit the registers of 16 lanes well.  Lane l of a group holds the V
+// consecutive logits [l*V, l*V + V), V the smallest power of two with G*V >= E, so
+// the lowest lane that holds a value also holds its lowest expert id.  Each lane
+// sorts its logits once, as ordered integer keys, equal ones by id.  A choice is then
+// one maximum over the heads of the group's lanes and a pop of the list it came
+// from; K choices need no memory.  The softmax follows in the same registers: with m
+// the largest logit, p_j = exp(l_j - m) / sum.
 //
-// The launch is bound by the vector instructions of its waves, not by memory.
+// The launch is bound by the vector instructions of its waves, not by memory: one
+// round of the choice costs about V + 10 of them for all tokens of the wave.
 #include "train_device.hpp"
 
 namespace moe {
 
 namespace {
 
-constexpr int kGateWaves = 4;                       // tokens per workgroup
+constexpr int kGateWaves = 4;
 constexpr int kGateThreads = kGateWaves * kWave;
 
 // f32 -> int32 so that integer order is value order: -inf lowest, -0 equal to
@@ -104,19 +107,58 @@ __device__ __forceinline__ float exp_neg(float x) {
     return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f);
 }
 
-// What a lane has left to choose from.  head() is its largest key; find() says which
-// expert the wave's largest key m is and whether it is this lane's; pop() removes
-// this lane's head.
+// Reductions over the group of G lanes; every lane gets the result, and a sum has one
+// order.  16 lanes are one DPP row: pairs, quads, then mirrored halves.
+template <int G>
+struct Group;
+template <>
+struct Group<64> {
+    template <class T>
+    static __device__ __forceinline__ T max(T v) { return wave_max(v); }
+    static __device__ __forceinline__ float sum(float v) { return wave_sum(v); }
+    template <class T>
+    static __device__ __forceinline__ T share(T v, int k) { return readlane(v, k); }
+};
+template <>
+struct Group<16> {
+    template <class T, class Op>
+    static __device__ __forceinline__ T reduce(T v, Op op) {
+        v = op(v, other<0xB1>(v));    // lane ^ 1
+        v = op(v, other<0x4E>(v));    // lane ^ 2
+        v = op(v, other<0x141>(v));   // 7 - lane, of 8
+        return op(v, other<0x140>(v));   // 15 - lane
+    }
+    template <int CTRL, class T>
+    static __device__ __forceinline__ T other(T v) {
+        return __builtin_bit_cast(
+            T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+    }
+    static __device__ __forceinline__ int max(int v) {
+        return reduce(v, [](int a, int b) { return a > b ? a : b; });
+    }
+    static __device__ __forceinline__ float max(float v) {
+        return reduce(v, [](float a, float b) { return fmaxf(a, b); });
+    }
+    static __device__ __forceinline__ float sum(float v) {
+        return reduce(v, [](float a, float b) { return a + b; });
+    }
+    template <class T>
+    static __device__ __forceinline__ T share(T v, int k) { return __shfl(v, k, 16); }
+};
+
+// What a lane has left to choose from.  head() is its largest key, owns(m) whether the
+// group's largest key m is this lane's head, place() which of its logits the head
+// is; pop() removes it.
 
 // bf16: the low half of a key is free for the id, inverted, so keys differ and ties
 // go to the lowest id by themselves.  Sorted once by the odd-even merge network.
 template <int V>
 struct PackedList {
     int key[V];
-    __device__ __forceinline__ PackedList(const float (&v)[V], int lane) {
+    __device__ __forceinline__ PackedList(const float (&v)[V], int gl) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            key[i] = (order_key(v[i]) & (int)0xffff0000) | (0xffff - (lane * V + i));
+            key[i] = (order_key(v[i]) & (int)0xffff0000) | (0xffff - (gl * V + i));
 #pragma unroll
         for (int p = 1; p < V; p <<= 1)
 #pragma unroll
@@ -132,10 +174,9 @@ struct PackedList {
                         }
     }
     __device__ __forceinline__ int head() const { return key[0]; }
-    __device__ __forceinline__ bool find(int m, int lane, int& expert) const {
-        expert = 0xffff - (m & 0xffff);
-        return key[0] == m;
-    }
+    template <int G>
+    __device__ __forceinline__ bool owns(int m) const { return key[0] == m; }
+    __device__ __forceinline__ int place() const { return (0xffff - (key[0] & 0xffff)) % V; }
     __device__ __forceinline__ void pop() {
 #pragma unroll
         for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
@@ -146,6 +187,16 @@ struct PackedList {
     }
 };
 
+// Whether this is the lowest lane of its group that says yes.
+template <int G>
+__device__ __forceinline__ bool lowest(bool yes) {
+    const uint64_t all = ballot64(yes);
+    if (G == 64) return yes && lanes_below(all) == 0;
+    const int row = (int)(threadIdx.x % kWave) & ~(G - 1);
+    const uint32_t mine = (uint32_t)(all >> row) & ((1u << G % 32) - 1u);
+    return yes && (mine & ((1u << (threadIdx.x % G)) - 1u)) == 0;
+}
+
 // f32: keys fill the word.  Sorted by neighbours, which keeps equal keys in order of
 // their ids, along with the places 0..V-1 they came from (4 bits each, the head's
 // lowest).
@@ -153,7 +204,7 @@ template <int V>
 struct FullList {
     static_assert(V <= 8, "places in one word");
     int key[V];
-    uint32_t place;
+    uint32_t places;
     __device__ __forceinline__ FullList(const float (&v)[V], int) {
         int from[V];
 #pragma unroll
@@ -174,21 +225,19 @@ struct FullList {
                 from[j] = fl;
             }
         }
-        place = 0;
+        places = 0;
 #pragma unroll
-        for (int i = V - 1; i >= 0; --i) place = place << 4 | (uint32_t)from[i];
+        for (int i = V - 1; i >= 0; --i) places = places << 4 | (uint32_t)from[i];
     }
     __device__ __forceinline__ int head() const { return key[0]; }
-    __device__ __forceinline__ bool find(int m, int lane, int& expert) const {
-        const int owner = __builtin_ctzll(ballot64(key[0] == m));
-        expert = owner * V + (int)(readlane(place, owner) & 15);
-        return lane == owner;
-    }
+    template <int G>
+    __device__ __forceinline__ bool owns(int m) const { return lowest<G>(key[0] == m); }
+    __device__ __forceinline__ int place() const { return (int)(places & 15); }
     __device__ __forceinline__ void pop() {
 #pragma unroll
         for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
         key[V - 1] = kTakenKey;
-        place >>= 4;
+        places >>= 4;
     }
     static __device__ __forceinline__ float value(int m) { return key_value(m); }
 };
@@ -215,11 +264,9 @@ struct FullScan {
             }
     }
     __device__ __forceinline__ int head() const { return best; }
-    __device__ __forceinline__ bool find(int m, int lane, int& expert) const {
-        const int owner = __builtin_ctzll(ballot64(best == m));
-        expert = owner * V + readlane(at, owner);
-        return lane == owner;
-    }
+    template <int G>
+    __device__ __forceinline__ bool owns(int m) const { return lowest<G>(best == m); }
+    __device__ __forceinline__ int place() const { return at; }
     __device__ __forceinline__ void pop() {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -246,56 +293,63 @@ struct LaneChoice<16, true> {
     using type = FullScan<16>;
 };
 
-template <int V, bool F32>
+// Tokens of the workgroup's wave, G lanes each; a wave whose last tokens are past T
+// computes token T - 1 there and stores nothing, so that every lane takes part.
+template <int G, int V, bool F32>
 __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a, bool vec) {
-    const int lane = threadIdx.x % kWave;
-    const int64_t step = (int64_t)gridDim.x * kGateWaves;
-    for (int64_t t = (int64_t)blockIdx.x * kGateWaves + threadIdx.x / kWave; t < a.T; t += step) {
+    constexpr int kTokens = kGateThreads / G;
+    const int gl = threadIdx.x % G;
+    for (int64_t b = blockIdx.x; b * kTokens < a.T; b += gridDim.x) {
+        const int64_t want = b * kTokens + threadIdx.x / G;
+        const bool live = want < a.T;
+        const int64_t t = live ? want : a.T - 1;
         float v[V];
-        load_logits<V, F32>(a.logits, t, a.E, lane, vec, v);
+        load_logits<V, F32>(a.logits, t, a.E, gl, vec, v);
         using Choice = typename LaneChoice<V, F32>::type;
-        Choice left(v, lane);
-        int my_idx = -1, my_key = kMaskedKey;    // lane k: choice k
+        Choice left(v, gl);
+        int my_key = kMaskedKey, top_key = kMaskedKey;   // lane k: choice k
         for (int k = 0; k < a.K; ++k) {
-            const int m = wave_max(left.head());
-            if (m <= kMaskedKey) break;          // the same in every lane
-            int expert;
-            const bool mine = left.find(m, lane, expert);
-            if (lane == k) {
-                my_idx = expert;
-                my_key = m;
+            const int m = Group<G>::max(left.head());
+            if (gl == k) my_key = m;
+            if (k == 0) top_key = m;
+            if (left.template owns<G>(m) && m > kMaskedKey) {
+                if (live) a.idx[t * a.K + k] = gl * V + left.place();
+                left.pop();
             }
-            if (mine) left.pop();
         }
-        const float top = Choice::value(readlane(my_key, 0));
-        const float e = my_idx >= 0 ? exp_neg(Choice::value(my_key) - top) : 0.0f;
+        const bool some = top_key > kMaskedKey, mine = my_key > kMaskedKey && gl < a.K;
+        const float top = Choice::value(top_key);
+        const float e = mine ? exp_neg(Choice::value(my_key) - top) : 0.0f;
         float part = e;
         if (!a.renorm) {
             part = 0.0f;
-            if (readlane(my_idx, 0) >= 0) {
+            if (some) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) part += exp_neg(v[i] - top);
             }
         }
-        const float total = wave_sum(part);
-        if (lane < a.K) {
-            a.idx[t * a.K + lane] = my_idx;
-            a.w[t * a.K + lane] = my_idx >= 0 ? (e / total) * a.scale : 0.0f;
+        const float total = Group<G>::sum(part);
+        if (gl < a.K && live) {
+            if (!mine) a.idx[t * a.K + gl] = -1;
+            a.w[t * a.K + gl] = mine ? (e / total) * a.scale : 0.0f;
         }
     }
 }
 
-template <int V, bool F32>
+template <int G, int V, bool F32>
 __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateArgs a, bool vec) {
-    const int lane = threadIdx.x % kWave;
-    const int64_t step = (int64_t)gridDim.x * kGateWaves;
-    for (int64_t t = (int64_t)blockIdx.x * kGateWaves + threadIdx.x / kWave; t < a.T; t += step) {
+    constexpr int kTokens = kGateThreads / G;
+    const int gl = threadIdx.x % G;
+    for (int64_t b = blockIdx.x; b * kTokens < a.T; b += gridDim.x) {
+        const int64_t want = b * kTokens + threadIdx.x / G;
+        const bool live = want < a.T;
+        const int64_t t = live ? want : a.T - 1;
         // lane k: entry k's expert, its logit and the gradient of its weight
         int j = -1;
         float l = -__builtin_inff(), dw = 0.0f;
-        if (lane < a.K) {
-            const int32_t id = a.idx[t * a.K + lane];
-            const float g = a.dw[t * a.K + lane];
+        if (gl < a.K) {
+            const int32_t id = a.idx[t * a.K + gl];
+            const float g = a.dw[t * a.K + gl];
             if (id >= 0 && id < a.E) {
                 j = id;
                 dw = g;
@@ -305,11 +359,11 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateArgs a,
         float v[V];
         float top = l;
         if (!a.renorm) {
-            load_logits<V, F32>(a.logits, t, a.E, lane, vec, v);
+            load_logits<V, F32>(a.logits, t, a.E, gl, vec, v);
 #pragma unroll
             for (int i = 0; i < V; ++i) top = fmaxf(top, v[i]);
         }
-        top = wave_max(top);
+        top = Group<G>::max(top);
         if (top == -__builtin_inff()) top = 0.0f;      // nothing to choose from: exp gives 0
         const float e = j >= 0 ? exp_neg(l - top) : 0.0f;
         float part = e;
@@ -321,45 +375,51 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateArgs a,
                 part += v[i];
             }
         }
-        float total = wave_sum(part);
+        float total = Group<G>::sum(part);
         if (total == 0.0f) total = 1.0f;
         const float p = e / total;
         const float d = j >= 0 ? (p * dw) * a.scale : 0.0f;
-        const float dot = wave_sum(d);
+        const float dot = Group<G>::sum(d);
         const float mine = a.renorm ? d - p * dot : d;
         float g[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) g[i] = a.renorm ? 0.0f : -((v[i] / total) * dot);
         // in order of k, so an expert named twice gets both in a fixed order
         for (int k = 0; k < a.K; ++k) {
-            const int jk = readlane(j, k);
-            if (jk < 0) continue;
-            const float x = readlane(mine, k);
-            if (lane != jk / V) continue;
+            const int jk = Group<G>::share(j, k);
+            const float x = Group<G>::share(mine, k);
+            const int at = jk - gl * V;    // no place of this lane where jk is -1
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (i == jk % V) g[i] += x;
+                if (jk >= 0 && at == i) g[i] += x;
         }
-        store_logits<V, F32>(a.dlogits, t, a.E, lane, vec, g);
+        if (live) store_logits<V, F32>(a.dlogits, t, a.E, gl, vec, g);
     }
 }
 
-template <int V, bool F32>
+template <int G, int V, bool F32>
 void go(const GateArgs& a, bool backward, hipStream_t s) {
-    const dim3 grid = capped_grid((a.T + kGateWaves - 1) / kGateWaves), block(kGateThreads);
+    constexpr int kTokens = kGateThreads / G;
+    const dim3 grid = capped_grid((a.T + kTokens - 1) / kTokens), block(kGateThreads);
     const uintptr_t at = (uintptr_t)a.logits | (uintptr_t)(backward ? a.dlogits : nullptr);
     const bool vec = a.E % V == 0 && at % 16 == 0;
-    if (backward) gate_backward_kernel<V, F32><<<grid, block, 0, s>>>(a, vec);
-    else gate_kernel<V, F32><<<grid, block, 0, s>>>(a, vec);
+    if (backward) gate_backward_kernel<G, V, F32><<<grid, block, 0, s>>>(a, vec);
+    else gate_kernel<G, V, F32><<<grid, block, 0, s>>>(a, vec);
 }
 
+// 16 lanes per token up to 128 f32 or 256 bf16 logits.  Measured at T=16384, us per
+// call, 64 lanes -> 16: bf16 E=64 7.3 -> 6.2, E=256 8.5 -> 6.1 (gradient 11.4 -> 9.4);
+// f32 E=64 7.8 -> 6.1, E=128 8.5 -> 6.6 (gradient 9.3 -> 7.2), but E=256 10.5 -> 11.2
+// (gradient 12.2 -> 13.5).
 template <bool F32>
 void by_e(const GateArgs& a, bool backward, hipStream_t s) {
-    if (a.E <= 64) go<1, F32>(a, backward, s);
-    else if (a.E <= 128) go<2, F32>(a, backward, s);
-    else if (a.E <= 256) go<4, F32>(a, backward, s);
-    else if (a.E <= 512) go<8, F32>(a, backward, s);
-    else go<16, F32>(a, backward, s);
+    if (a.E <= 16) return go<16, 1, F32>(a, backward, s);
+    if (a.E <= 32) return go<16, 2, F32>(a, backward, s);
+    if (a.E <= 64) return go<16, 4, F32>(a, backward, s);
+    if (a.E <= 128) return go<16, 8, F32>(a, backward, s);
+    if (a.E <= 256) return F32 ? go<64, 4, true>(a, backward, s) : go<16, 16, false>(a, backward, s);
+    if (a.E <= 512) return go<64, 8, F32>(a, backward, s);
+    go<64, 16, F32>(a, backward, s);
 }
 
 hipError_t launch(const GateArgs& a, bool backward, hipStream_t s) {

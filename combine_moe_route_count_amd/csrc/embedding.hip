@@ -148,18 +148,50 @@ __global__ __launch_bounds__(kEmbThreads) void move_kernel(MoveArgs a) {
     }
 }
 
-// Zeros into one chunk of table row v.  One non-temporal 16-byte store per lane and
-// many small workgroups: 7.0 TB/s, against 5.4-6.1 with four stores per lane, 3.9 to
-// 6.3 in a flat loop, and 4.5 with stores through L2 (131072 rows of 4096 f32).
+// Table rows to clear, kEmbThreads lane-units of 16 bytes per workgroup: several
+// narrow rows, or one chunk of a wide one.  One non-temporal store per lane and many
+// small workgroups: 7.0 TB/s, against 5.4-6.1 with four stores per lane, 3.9 to 6.3
+// in a flat loop, and 4.5 with stores through L2 (131072 rows of 4096 f32).
 constexpr int zero_unit(bool f32) { return f32 ? 4 : 8; }
+
+struct ZeroRows {
+    int units;     // lane-units of a row
+    int rows;      // rows per workgroup, if a row is narrow (else 1)
+    int chunks;    // workgroups per row, if it is wide (else 1)
+    int64_t blocks;
+};
+
+ZeroRows zero_layout(int64_t V, int64_t H, bool f32) {
+    ZeroRows z;
+    z.units = (int)(H / zero_unit(f32));
+    z.rows = z.units < kEmbThreads ? kEmbThreads / z.units : 1;
+    z.chunks = (z.units + kEmbThreads - 1) / kEmbThreads;
+    z.blocks = (V + z.rows - 1) / z.rows * z.chunks;
+    return z;
+}
+
+// The lane's row and unit of block b; false if it has none.
+__device__ __forceinline__ bool zero_place(const ZeroRows& z, int64_t b, int64_t V, int64_t& v,
+                                           int& u) {
+    const int tid = threadIdx.x;
+    if (z.chunks > 1 || z.rows == 1) {
+        v = b / z.chunks;
+        u = (int)(b - v * z.chunks) * kEmbThreads + tid;
+        return u < z.units;
+    }
+    const int r = tid / z.units;
+    v = b * z.rows + r;
+    u = tid - r * z.units;
+    return r < z.rows && v < V;
+}
+
 template <bool OF32>
-__device__ __forceinline__ void zero_row(void* table, int64_t H, int64_t v, int chunk) {
+__device__ __forceinline__ void zero_store(void* table, int64_t H, int64_t v, int u) {
     constexpr int EL = zero_unit(OF32);
-    const int64_t u = (int64_t)chunk * blockDim.x + threadIdx.x;
     float z[EL];
 #pragma unroll
     for (int j = 0; j < EL; ++j) z[j] = 0.0f;
-    if (u < H / EL) store_unit<OF32, true>(table, v * H + u * EL, z);
+    store_unit<OF32, true>(table, v * H + (int64_t)u * EL, z);
 }
 
 // Sort of up to kSmallSort ids by counting: position n goes behind every smaller id
@@ -181,19 +213,19 @@ struct SmallSortArgs {
     int32_t* total;
     void* dtable;
     int sort_blocks;
-    int64_t zero_blocks;
-    int zero_chunks;
+    ZeroRows zero;      // no blocks when accumulating
 };
 
 template <bool OF32>
 __global__ __launch_bounds__(kEmbThreads) void small_sort_kernel(SmallSortArgs a) {
     __shared__ __align__(16) int32_t key[kSmallSort];
     const int tid = threadIdx.x;
-    for (int64_t b = blockIdx.x; b < a.sort_blocks + a.zero_blocks; b += gridDim.x) {
+    for (int64_t b = blockIdx.x; b < a.sort_blocks + a.zero.blocks; b += gridDim.x) {
         if (b >= a.sort_blocks) {
-            const int64_t z = b - a.sort_blocks;
-            const int64_t v = z / a.zero_chunks;
-            zero_row<OF32>(a.dtable, a.H, v, (int)(z - v * a.zero_chunks));
+            int64_t v;
+            int u;
+            if (zero_place(a.zero, b - a.sort_blocks, a.V, v, u))
+                zero_store<OF32>(a.dtable, a.H, v, u);
             continue;
         }
         // ids of no row sort last and are not placed
@@ -252,11 +284,13 @@ struct SumArgs {
 template <bool OF32>
 __global__ __launch_bounds__(kEmbThreads) void zero_rows_kernel(void* table, int64_t V, int64_t H,
                                                                 const uint8_t* present,
-                                                                const int32_t* off, int nch) {
-    for (int64_t z = blockIdx.x; z < V * nch; z += gridDim.x) {
-        const int64_t v = z / nch;
+                                                                const int32_t* off, ZeroRows z) {
+    for (int64_t b = blockIdx.x; b < z.blocks; b += gridDim.x) {
+        int64_t v;
+        int u;
+        if (!zero_place(z, b, V, v, u)) continue;
         const bool some = present ? present[v] != 0 : off[v + 1] != off[v];
-        if (!some) zero_row<OF32>(table, H, v, (int)(z - v * nch));
+        if (!some) zero_store<OF32>(table, H, v, u);
     }
 }
 
@@ -337,7 +371,9 @@ __global__ __launch_bounds__(kEmbThreads) void windows_kernel(SumArgs a) {
 }
 
 // Runs that cross windows: workgroup (window in which the run begins, chunk) adds the
-// parts in order.
+// parts in order.  Letting the waves share the parts of a long run (sums of stretches
+// through LDS) was slower everywhere, its registers and LDS cost the short ones more:
+// 65536 tokens 496 -> 525 us, 8192 tokens over 200 rows 37 -> 42.
 template <bool OF32>
 __global__ __launch_bounds__(kEmbThreads) void join_kernel(SumArgs a, int nch) {
     constexpr int EL = 4;
@@ -389,12 +425,13 @@ __global__ __launch_bounds__(kEmbThreads) void join_kernel(SumArgs a, int nch) {
 }
 
 // Positions per window: 64 (one wave's lanes), fewer while there would be less than
-// kWantGroups workgroups of 2048 elements.  8192 tokens of 4096 over 200 rows: 34 us
-// with 512, 38 with 1024, 46 with 2048; 4096 tokens over 50000 rows 150, 153, 153.
-constexpr int64_t kWantGroups = 512;
+// kWantWaves waves of 512 elements.  8192 tokens of 1024 over 100 rows: 29.6 us with
+// 1024, 37.4 with 2048 or 4096; of 4096 over 200 rows 37.1, 34.1, 38.4; 65536 tokens
+// of 264 92, 93, 106.
+constexpr int64_t kWantWaves = 1024;
 inline int window_of(int64_t N, int64_t H) {
     int w = kWave;
-    while (w > 8 && (N + w - 1) / w * ((H + 2047) / 2048) < kWantGroups) w /= 2;
+    while (w > 8 && (N + w - 1) / w * ((H + 511) / 512) < kWantWaves) w /= 2;
     return w;
 }
 
@@ -467,10 +504,10 @@ hipError_t small_sort(const EmbeddingGradArgs& g, const SumArgs& a, hipStream_t 
     m.total = const_cast<int32_t*>(a.total);
     m.dtable = g.dtable;
     m.sort_blocks = (int)((g.N + kSortPositions - 1) / kSortPositions);
-    m.zero_chunks = chunks(g.H / zero_unit(OF32), kEmbThreads);
-    m.zero_blocks = g.accumulate ? 0 : g.V * m.zero_chunks;
+    m.zero = zero_layout(g.V, g.H, OF32);
+    if (g.accumulate) m.zero.blocks = 0;
     small_sort_kernel<OF32>
-        <<<capped_grid(m.sort_blocks + m.zero_blocks), dim3(kEmbThreads), 0, s>>>(m);
+        <<<capped_grid(m.sort_blocks + m.zero.blocks), dim3(kEmbThreads), 0, s>>>(m);
     return hipGetLastError();
 }
 
@@ -552,11 +589,10 @@ hipError_t grad_go(const EmbeddingGradArgs& g, hipStream_t s) {
     const int threads = row_threads(units, kEmbThreads);
     a.nch = chunks(units, threads);
     if (w.passes > 0 && !g.accumulate) {
-        const int zt = row_threads(g.H / zero_unit(OF32), kEmbThreads);
-        const int zch = chunks(g.H / zero_unit(OF32), zt);
-        zero_rows_kernel<OF32><<<capped_grid(g.V * zch), dim3(zt), 0, s>>>(
+        const ZeroRows z = zero_layout(g.V, g.H, OF32);
+        zero_rows_kernel<OF32><<<capped_grid(z.blocks), dim3(kEmbThreads), 0, s>>>(
             g.dtable, g.V, g.H, w.passes > 1 ? at<uint8_t>(g.ws, w.present) : nullptr,
-            at<int32_t>(g.ws, w.off0), zch);
+            at<int32_t>(g.ws, w.off0), z);
     }
     windows_kernel<DF32, OF32><<<capped_grid(a.windows * a.nch), dim3(threads), 0, s>>>(a);
     if (a.windows > 1) {

@@ -175,7 +175,7 @@ def combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], tok_map: tor
         _gpu("y", y, 2)
         rows = y.shape[0]
         quant = y.dtype in _QUANT
-        _need(quant or not fp4, "fp4 rows are uint8 codes")
+        _need(y.dtype == torch.uint8 or not fp4, "fp4 rows are uint8 codes")
         _tensor("y", y, (rows, H // 2 if fp4 else H), _QUANT if quant else _FLOAT, dev)
         y_dt = MOE_FP4_E2M1 if fp4 else (MOE_FP8_E4M3 if quant else _FLOAT[y.dtype])
     elif dy is not None:

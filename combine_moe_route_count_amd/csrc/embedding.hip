@@ -313,11 +313,15 @@ __device__ __forceinline__ void put_row(const SumArgs& a, int64_t v, int64_t col
     store_unit<OF32, false>(a.g.dtable, at, r);
 }
 
-// Windows: workgroup (window, chunk).
+// Windows: workgroup (window, chunk).  16-byte stores: units of 4 elements where the
+// table is f32 (161 us at 65536 tokens of 4096 bf16, 178 with units of 8), else of 8
+// (60 against 62 us at 32768 tokens into bf16).  Streamed row loads; through the caches
+// 176 and 71 us.
+constexpr int window_unit(bool dout_f32, bool table_f32) { return dout_f32 || table_f32 ? 4 : 8; }
 constexpr int kBatch = 8;   // rows in flight
 template <bool DF32, bool OF32>
 __global__ __launch_bounds__(kEmbThreads) void windows_kernel(SumArgs a) {
-    constexpr int EL = DF32 ? 4 : 8;   // one 16-byte load
+    constexpr int EL = window_unit(DF32, OF32);
     const int lane = threadIdx.x % kWave;
     const int units = (int)(a.g.H / EL);
     const int64_t m = *a.total;
@@ -462,12 +466,14 @@ GradWs grad_ws(int64_t N, int64_t V, int64_t H) {
         return at;
     };
     const size_t n = (size_t)N, nk = (size_t)1 << w.bits;
+    // the routing's arrival ticket first: calls of any size that share a workspace
+    // find it where the last one left it
+    w.ticket = take(sizeof(uint64_t));
     w.off0 = take(4 * (nk + 1));   // its last word: how many ids are valid
     w.id[0] = take(4 * n);
     w.pos[0] = take(4 * n);
     w.partial = take(4 * 2 * (size_t)w.windows * (size_t)H);
     if (w.passes > 0) {
-        w.ticket = take(sizeof(uint64_t));
         w.local_rank = take(4 * n);
         w.tile_cnt = take(4 * (size_t)w.tiles * nk);
         w.tile_flags = take(8 * (size_t)w.tiles);
@@ -585,7 +591,7 @@ hipError_t grad_go(const EmbeddingGradArgs& g, hipStream_t s) {
         const hipError_t e = small_sort<OF32>(g, a, s);
         if (e != hipSuccess || g.N == 0) return e;
     }
-    const int64_t units = g.H / (DF32 ? 4 : 8);
+    const int64_t units = g.H / window_unit(DF32, OF32);
     const int threads = row_threads(units, kEmbThreads);
     a.nch = chunks(units, threads);
     if (w.passes > 0 && !g.accumulate) {

@@ -179,6 +179,18 @@ def test_messages_name_the_argument(res):
     assert "id_bytes=2" in res["embedding"]["ib"][1]
 
 
+def test_binding_refuses_tensors_off_the_gpu():
+    import torch
+    import combine_moe_route_count_amd as moe
+    f, i, m = torch.zeros((4, 8)), torch.zeros(4, dtype=torch.int32), torch.zeros((4, 2), dtype=torch.int64)
+    for call in (lambda: moe.gate(f, 2), lambda: moe.gate_backward(f, m.int(), torch.zeros((4, 2))),
+                 lambda: moe.combine_backward(f, f, m, torch.zeros((4, 2))),
+                 lambda: moe.dispatch_backward(f, m), lambda: moe.embedding(i, f),
+                 lambda: moe.embedding_backward(f, i, 8)):
+        with pytest.raises(ValueError, match="not on a GPU"):
+            call()
+
+
 def test_host_code_under_asan_ubsan(tmp_path):
     from combine_moe_route_count_amd import build
     san_src = [s for s in build.SOURCES if s.startswith("api")]

@@ -15,6 +15,11 @@
 // The sort: up to kSmallSort positions are ranked by counting, one launch.  More are
 // radix sorted; a digit (at most 9 bits) is the key of the one-launch routing
 // (route_fused.hip), so a pass is its stable slots and the move of (id, position).
+//
+// What bounds it: one read of dout's rows and one write of the table, most of it zeros
+// for a large vocabulary.  65536 tokens of 4096 (bf16, Zipf) into 131072 f32 rows, 2.66
+// GB: 474 us = 5.6 TB/s, of it zeros 260 us (7.0 TB/s), windows 161 (5.2 TB/s), sort 37
+// and join 15.
 #include "train_device.hpp"
 #include "internal.hpp"
 
@@ -115,39 +120,6 @@ void embedding_go(const EmbeddingArgs& a, hipStream_t s) {
 // ---------------------------------------------------------------------------
 // gradient: the sort
 // ---------------------------------------------------------------------------
-struct MoveArgs {              // one radix pass's move
-    DigitSource d;
-    int64_t N;
-    const int32_t* local_rank;
-    const int32_t* tile_base;  // [tiles][NK]
-    const int32_t* off;        // [NK+1]
-    int NK;
-    const int32_t* in_pos;     // null: the position is the entry's own number
-    int32_t* out_id;
-    int32_t* out_pos;
-    uint8_t* clear;            // first of several passes: [V] flags to clear, or null
-    uint8_t* present;          // last of several passes: flags of the ids that occur, or null
-    int64_t V;
-};
-
-__global__ __launch_bounds__(kEmbThreads) void move_kernel(MoveArgs a) {
-    const int64_t step = (int64_t)gridDim.x * kEmbThreads;
-    const int64_t first = (int64_t)blockIdx.x * kEmbThreads + threadIdx.x;
-    if (a.clear)
-        for (int64_t v = first; v < a.V; v += step) a.clear[v] = 0;
-    for (int64_t f = first; f < a.N; f += step) {
-        const int32_t lr = a.local_rank[f];
-        if (lr < 0) continue;
-        const int32_t id = a.d.total ? ((const int32_t*)a.d.ids)[f]
-                                     : (int32_t)token_id(a.d.ids, a.d.id_bytes, f);
-        const int key = (id >> a.d.shift) & a.d.mask;
-        const int64_t to = (int64_t)a.off[key] + a.tile_base[(f / kTile) * a.NK + key] + lr;
-        a.out_id[to] = id;
-        a.out_pos[to] = a.in_pos ? a.in_pos[f] : (int32_t)f;
-        if (a.present) a.present[id] = 1;
-    }
-}
-
 // Table rows to clear, kEmbThreads lane-units of 16 bytes per workgroup: several
 // narrow rows, or one chunk of a wide one.  One non-temporal store per lane and many
 // small workgroups: 7.0 TB/s, against 5.4-6.1 with four stores per lane, 3.9 to 6.3
@@ -192,6 +164,53 @@ __device__ __forceinline__ void zero_store(void* table, int64_t H, int64_t v, in
 #pragma unroll
     for (int j = 0; j < EL; ++j) z[j] = 0.0f;
     store_unit<OF32, true>(table, v * H + (int64_t)u * EL, z);
+}
+
+struct MoveArgs {              // one radix pass's move
+    DigitSource d;
+    int64_t N;
+    const int32_t* local_rank;
+    const int32_t* tile_base;  // [tiles][NK]
+    const int32_t* off;        // [NK+1]
+    int NK;
+    const int32_t* in_pos;     // null: the position is the entry's own number
+    int32_t* out_id;
+    int32_t* out_pos;
+    uint8_t* clear;            // first of several passes: [V] flags to clear, or null
+    uint8_t* present;          // last of several passes: flags of the ids that occur, or null
+    int64_t V;
+    void* dtable;              // table to zero by the workgroups past move_blocks, or null
+    bool dtable_f32;
+    int64_t H;
+    int64_t move_blocks;
+    ZeroRows zero;
+};
+
+__global__ __launch_bounds__(kEmbThreads) void move_kernel(MoveArgs a) {
+    for (int64_t b = (int64_t)blockIdx.x - a.move_blocks; a.dtable && b < a.zero.blocks;
+         b += gridDim.x) {
+        int64_t v;
+        int u;
+        if (b < 0 || !zero_place(a.zero, b, a.V, v, u)) continue;
+        if (a.dtable_f32) zero_store<true>(a.dtable, a.H, v, u);
+        else zero_store<false>(a.dtable, a.H, v, u);
+    }
+    if (blockIdx.x >= a.move_blocks) return;
+    const int64_t step = a.move_blocks * kEmbThreads;
+    const int64_t first = (int64_t)blockIdx.x * kEmbThreads + threadIdx.x;
+    if (a.clear)
+        for (int64_t v = first; v < a.V; v += step) a.clear[v] = 0;
+    for (int64_t f = first; f < a.N; f += step) {
+        const int32_t lr = a.local_rank[f];
+        if (lr < 0) continue;
+        const int32_t id = a.d.total ? ((const int32_t*)a.d.ids)[f]
+                                     : (int32_t)token_id(a.d.ids, a.d.id_bytes, f);
+        const int key = (id >> a.d.shift) & a.d.mask;
+        const int64_t to = (int64_t)a.off[key] + a.tile_base[(f / kTile) * a.NK + key] + lr;
+        a.out_id[to] = id;
+        a.out_pos[to] = a.in_pos ? a.in_pos[f] : (int32_t)f;
+        if (a.present) a.present[id] = 1;
+    }
 }
 
 // Sort of up to kSmallSort ids by counting: position n goes behind every smaller id
@@ -445,7 +464,15 @@ struct GradWs {
     int64_t tiles, windows;
     int passes, bits;   // digits, and bits of each; no pass: the small sort
     int window;
+    bool zero_early;
 };
+
+// Up to this many bytes of rows of tokens that occur (at most min(N,V) rows, as f32),
+// the whole table is zeroed beside the first move and those rows are written twice;
+// past it, the rows of absent tokens get a launch of their own that writes nothing
+// twice.  10136 tokens of 80 into 8762 bf16 rows: 39.2 us beside the move, 41.6 apart;
+// 65536 of 64 into 131072 f32 rows 64.0, 67.6; 8192 of 4096 into 50000 rows 164, 159.
+constexpr int64_t kZeroTwice = (int64_t)64 << 20;
 
 GradWs grad_ws(int64_t N, int64_t V, int64_t H) {
     GradWs w{};
@@ -458,6 +485,7 @@ GradWs grad_ws(int64_t N, int64_t V, int64_t H) {
         const int most = digit_bits(w.tiles);
         w.passes = (bits + most - 1) / most;
         w.bits = (bits + w.passes - 1) / w.passes;
+        w.zero_early = (N < V ? N : V) * H * 4 <= kZeroTwice;
     }
     size_t total = 0;
     auto take = [&total](size_t bytes) {
@@ -493,7 +521,10 @@ P* at(void* ws, size_t off) {
     return (P*)((char*)ws + off);
 }
 
-inline dim3 flat_grid(int64_t n) { return capped_grid((n + kEmbThreads - 1) / kEmbThreads); }
+inline int64_t flat_blocks(int64_t n) {
+    const int64_t b = (n + kEmbThreads - 1) / kEmbThreads;
+    return b < kMaxGrid ? b : kMaxGrid;
+}
 
 inline int chunks(int64_t units, int threads) { return (int)((units + threads - 1) / threads); }
 
@@ -562,10 +593,21 @@ hipError_t radix_sort(const EmbeddingGradArgs& g, const GradWs& w, int& cur, hip
         m.in_pos = p == 0 ? nullptr : at<int32_t>(ws, w.pos[cur]);
         m.out_id = at<int32_t>(ws, w.id[next]);
         m.out_pos = at<int32_t>(ws, w.pos[next]);
-        if (w.passes > 1 && p == 0) m.clear = at<uint8_t>(ws, w.present);
-        if (w.passes > 1 && p == w.passes - 1) m.present = at<uint8_t>(ws, w.present);
         m.V = g.V;
-        move_kernel<<<flat_grid(m.clear && g.V > g.N ? g.V : g.N), dim3(kEmbThreads), 0, s>>>(m);
+        m.H = g.H;
+        if (w.zero_early && !g.accumulate) {
+            if (p == 0) {
+                m.dtable = g.dtable;
+                m.dtable_f32 = g.dtable_f32;
+                m.zero = zero_layout(g.V, g.H, g.dtable_f32);
+            }
+        } else if (w.passes > 1) {
+            if (p == 0) m.clear = at<uint8_t>(ws, w.present);
+            if (p == w.passes - 1) m.present = at<uint8_t>(ws, w.present);
+        }
+        m.move_blocks = flat_blocks(m.clear && g.V > g.N ? g.V : g.N);
+        move_kernel<<<capped_grid(m.move_blocks + (m.dtable ? m.zero.blocks : 0)),
+                      dim3(kEmbThreads), 0, s>>>(m);
         cur = next;
     }
     return hipGetLastError();
@@ -594,7 +636,7 @@ hipError_t grad_go(const EmbeddingGradArgs& g, hipStream_t s) {
     const int64_t units = g.H / window_unit(DF32, OF32);
     const int threads = row_threads(units, kEmbThreads);
     a.nch = chunks(units, threads);
-    if (w.passes > 0 && !g.accumulate) {
+    if (w.passes > 0 && !w.zero_early && !g.accumulate) {
         const ZeroRows z = zero_layout(g.V, g.H, OF32);
         zero_rows_kernel<OF32><<<capped_grid(z.blocks), dim3(kEmbThreads), 0, s>>>(
             g.dtable, g.V, g.H, w.passes > 1 ? at<uint8_t>(g.ws, w.present) : nullptr,

@@ -143,6 +143,50 @@ def test_gate_nan_and_infinities():
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("E", [8, 60, 64, 128, 256, 512, 1024])
+def test_gate_on_unaligned_logits(E, dt):
+    """Rows whose vectors straddle 16 bytes give the same bits as aligned ones."""
+    note(f"gate unaligned {E} {dt}")
+    T, K = 37, 6
+    g = _gen(E)
+    l = _randn(g, (T, E), dt, 2.0)
+    odd = torch.empty(T * E + 1, dtype=dt, device=DEV)[1:].view(T, E)
+    odd.copy_(l)
+    dw = _randn(g, (T, K))
+    for renorm in (True, False):
+        a, b = moe.gate(l, K, renormalize=renorm), moe.gate(odd, K, renormalize=renorm)
+        _same(a[0], b[0], "idx")
+        _same(a[1], b[1], "w")
+        want = moe.gate_backward(l, a[0], dw, renormalize=renorm)
+        got = torch.empty(T * E + 1, dtype=dt, device=DEV)[1:].view(T, E)
+        _same(moe.gate_backward(odd, a[0], dw, renormalize=renorm, dlogits=got), want, "dlogits")
+        _same(moe.gate_backward(odd, a[0], dw, renormalize=renorm), want, "dlogits, one side")
+
+
+def test_nothing_to_do():
+    """No tokens, no rows: empty outputs, and rows without entries are still zeroed."""
+    note("empty")
+    z = lambda *s, dt=F32: torch.zeros(s, dtype=dt, device=DEV)                     # noqa: E731
+    idx, w = moe.gate(z(0, 8), 2)
+    assert idx.shape == (0, 2) and w.shape == (0, 2)
+    assert moe.gate_backward(z(0, 8), idx, w).shape == (0, 8)
+    tm = z(0, 2, dt=torch.int64)
+    assert moe.dispatch_backward(z(0, 16), tm).shape == (0, 16)
+    dy, dw = moe.combine_backward(z(0, 16), z(5, 16), tm, w)
+    assert dy.shape == (5, 16) and dw.shape == (0, 2)
+    dy = torch.full((5, 16), 3.0, device=DEV)
+    moe.combine_backward(z(0, 16), z(5, 16), tm, w, dy=dy, packed_cnt=z(2, dt=torch.int32),
+                         packed_off=z(3, dt=torch.int32))
+    assert (dy == 0).all()
+    dy, dw = moe.combine_backward(torch.ones((3, 16), device=DEV), z(0, 16), torch.full((3, 2), -1, device=DEV),
+                                  torch.ones((3, 2), device=DEV))
+    assert dy.shape == (0, 16) and (dw == 0).all()
+    assert (moe.dispatch_backward(z(0, 16), torch.full((3, 2), -1, device=DEV)) == 0).all()
+    assert moe.embedding(z(0, dt=torch.int32), z(4, 8)).shape == (0, 8)
+    assert (moe.embedding_backward(z(0, 8), z(0, dt=torch.int64), 4) == 0).all()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("T,E,K", GATE_SHAPES)
 @pytest.mark.parametrize("kind", ["normal", "masked"])
 def test_gate_backward(T, E, K, dt, kind):
@@ -467,7 +511,10 @@ GRAD = [(1, 1, 8, "uniform"), (0, 9, 16, "uniform"), (1, 600, 7168, "uniform"), 
         (63, 10, 520, "zipf"), (64, 513, 8, "distinct"), (255, 3, 128, "zipf"), (256, 300, 256, "same"),
         (257, 300, 256, "same"), (300, 5000, 1000, "padded"), (777, 65537, 64, "zipf"),
         (1024, 200, 2048, "padded"), (1025, 40, 4104, "runs"), (2500, 2, 72, "runs"), (3000, 131072, 16, "zipf"),
-        (4099, 1000, 136, "same"), (5000, 262145, 8, "zipf"), (9000, 50, 64, "runs"), (20000, 3000, 48, "zipf")]
+        (4099, 1000, 136, "same"), (5000, 262145, 8, "zipf"), (9000, 50, 64, "runs"), (20000, 3000, 48, "zipf"),
+        (4096, 700, 64, "zipf"), (4097, 512, 8, "padded"), (4100, 500, 33016, "padded"),
+        (5000, 6001, 4104, "zipf"), (4608, 9, 24, "same"), (70000, 200, 8, "zipf"),
+        (300000, 5000, 8, "runs")]
 
 
 def _grad_ref(dout, ids, V, scale):
@@ -589,9 +636,9 @@ def _everything(c, o):
 
 
 def _everything_inputs(seed):
-    T, H, E, K, V = 3000, 520, 32, 4, 700
+    T, H, E, K, V = 6000, 520, 32, 4, 700      # past 4096 positions: sorted by digits
     g = _gen(seed)
-    idx, d, rows = _routing(g, T, E, K, 500)
+    idx, d, rows = _routing(g, T, E, K, 1000)
     c = dict(K=K, V=V, logits=_randn(g, (T, E)), idx=idx, dw=_randn(g, (T, K)), dout=_randn(g, (T, H), BF16),
              y=_randn(g, (rows, H), BF16), tm=d.tok_map, w=torch.rand((T, K), generator=g).to(DEV),
              pc=d.packed_cnt, po=d.packed_off, ids=_ids(g, T, V, "zipf", torch.int64),
@@ -633,6 +680,34 @@ def test_captured_in_a_graph():
         for k in ref:
             _same(o[k], ref[k], f"replay {i}: {k}")
             _same(other[k], ref[k], f"eager {i}: {k}")
+
+
+def test_two_graphs_on_one_workspace():
+    """Two captured graphs whose sorts take other sizes and numbers of passes, replayed in turn on
+    one stream with one workspace between them."""
+    note("two graphs")
+    g = _gen(61)
+    a = dict(V=700, ids=_ids(g, 6000, 700, "zipf", torch.int64), dout=_randn(g, (6000, 264), BF16))
+    b = dict(V=300001, ids=_ids(g, 9000, 300001, "zipf", torch.int32), dout=_randn(g, (9000, 8), BF16))
+    size = max(moe.embedding_workspace_size(c["dout"].shape[0], c["V"], c["dout"].shape[1]) for c in (a, b))
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    graphs = []
+    for c in (a, b):
+        c["ref"] = moe.embedding_backward(c["dout"], c["ids"], c["V"])
+        c["out"] = torch.empty_like(c["ref"])
+        moe.embedding_backward(c["dout"], c["ids"], c["V"], dtable=c["out"], ws=ws)
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            moe.embedding_backward(c["dout"], c["ids"], c["V"], dtable=c["out"], ws=ws)
+        graphs.append(gr)
+    for i in range(4):
+        for c in (a, b):
+            c["out"].fill_(float("nan"))
+        for gr in graphs:
+            gr.replay()
+        for c in (a, b):
+            _same(c["out"], c["ref"], f"replay {i}")
 
 
 def test_two_streams():

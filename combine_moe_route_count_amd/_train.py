@@ -63,9 +63,8 @@ def _need(cond: bool, msg: str) -> None:
 # dev is a device index.
 def _tensor(name: str, t: torch.Tensor, shape, dtypes, dev: int) -> None:
     """t is a contiguous tensor of this shape, one of these types, on GPU dev."""
-    if (t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev
-            and t.is_cuda):
-        return
+    if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return   # (a tensor off the GPU has device -1)
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has type {t.dtype}, not one of {[str(d) for d in dtypes]}")
     if t.shape != shape:
@@ -82,6 +81,14 @@ def _gpu(name: str, t: torch.Tensor, dim: int) -> int:
     if t.dim() != dim:
         raise ValueError(f"{name} has {t.dim()} dimensions, not {dim}")
     return t.get_device()
+
+
+def _dim(name: str, t: torch.Tensor, dims: int, which: int) -> int:
+    """Size `which` of t, which has `dims` dimensions."""
+    shape = t.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} has {len(shape)} dimensions, not {dims}")
+    return shape[which]
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -132,9 +139,8 @@ def gate_backward(logits: torch.Tensor, idx: torch.Tensor, dw: torch.Tensor,
     """Gradient of gate's weights with respect to the logits, the choice idx held
     fixed: dlogits [T,E] of the logits' type."""
     dev = _gpu("logits", logits, 2)
-    _gpu("idx", idx, 2)
     T, E = logits.shape
-    K = idx.shape[1]
+    K = _dim("idx", idx, 2, 1)
     _tensor("logits", logits, (T, E), _FLOAT, dev)
     _tensor("idx", idx, (T, K), (torch.int32,), dev)
     _tensor("dw", dw, (T, K), (torch.float32,), dev)
@@ -164,23 +170,20 @@ def combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], tok_map: tor
     written.  want_dy / want_dw leave one of the two out (y may be None without dw
     if dy is given, w without dy)."""
     dev = _gpu("dout", dout, 2)
-    _gpu("tok_map", tok_map, 2)
     T, H = dout.shape
-    K = tok_map.shape[1]
+    K = _dim("tok_map", tok_map, 2, 1)
     _need(want_dy or want_dw, "neither dy nor dw is wanted")
     _tensor("dout", dout, (T, H), _FLOAT, dev)
     _tensor("tok_map", tok_map, (T, K), (torch.int64,), dev)
     y_dt, rows = MOE_BF16, 0
     if y is not None:
-        _gpu("y", y, 2)
-        rows = y.shape[0]
+        rows = _dim("y", y, 2, 0)
         quant = y.dtype in _QUANT
         _need(y.dtype == torch.uint8 or not fp4, "fp4 rows are uint8 codes")
         _tensor("y", y, (rows, H // 2 if fp4 else H), _QUANT if quant else _FLOAT, dev)
         y_dt = MOE_FP4_E2M1 if fp4 else (MOE_FP8_E4M3 if quant else _FLOAT[y.dtype])
     elif dy is not None:
-        _gpu("dy", dy, 2)
-        rows = dy.shape[0]
+        rows = _dim("dy", dy, 2, 0)
     _need(y is not None or not want_dw, "dw needs y")
     _need(y is not None or dy is not None, "without y, dy must be given")
     if y_scales is not None:
@@ -190,8 +193,7 @@ def combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], tok_map: tor
     _need((packed_cnt is None) == (packed_off is None), "packed_cnt and packed_off go together")
     E = 0
     if packed_cnt is not None:
-        _gpu("packed_cnt", packed_cnt, 1)
-        E = packed_cnt.shape[0]
+        E = _dim("packed_cnt", packed_cnt, 1, 0)
         _tensor("packed_cnt", packed_cnt, (E,), (torch.int32,), dev)
         _tensor("packed_off", packed_off, (E + 1,), (torch.int32,), dev)
     if want_dy:
@@ -229,9 +231,8 @@ def dispatch_backward(dpacked: torch.Tensor, tok_map: torch.Tensor,
     residual's type, or dpacked's, unless dx or dx_dtype says otherwise; residual
     may be dx itself."""
     dev = _gpu("dpacked", dpacked, 2)
-    _gpu("tok_map", tok_map, 2)
     rows, H = dpacked.shape
-    T, K = tok_map.shape
+    T, K = _dim("tok_map", tok_map, 2, 0), tok_map.shape[1]
     _tensor("dpacked", dpacked, (rows, H), _FLOAT, dev)
     _tensor("tok_map", tok_map, (T, K), (torch.int64,), dev)
     if dx is None:
@@ -252,9 +253,8 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0,
     outside the table (-1 is "no token"; any other is counted into stats int32 [1]
     if given)."""
     dev = _gpu("table", table, 2)
-    _gpu("ids", ids, 1)
     V, H = table.shape
-    N = ids.shape[0]
+    N = _dim("ids", ids, 1, 0)
     _tensor("table", table, (V, H), _FLOAT, dev)
     _tensor("ids", ids, (N,), _IDS, dev)
     if out is None:
@@ -289,8 +289,8 @@ def embedding_backward(dout: torch.Tensor, ids: torch.Tensor, V: int, scale: flo
     accumulate=True adds to dtable (which must be given) and leaves the rows of
     tokens that do not occur alone."""
     dev = _gpu("dout", dout, 2)
-    _gpu("ids", ids, 1)
     N, H = dout.shape
+    _dim("ids", ids, 1, 0)
     _tensor("dout", dout, (N, H), _FLOAT, dev)
     _tensor("ids", ids, (N,), _IDS, dev)
     _need(dtable is not None or not accumulate, "accumulate needs dtable")

@@ -407,17 +407,25 @@ void go(const GateArgs& a, bool backward, hipStream_t s) {
     else gate_kernel<G, V, F32><<<grid, block, 0, s>>>(a, vec);
 }
 
-// 16 lanes per token up to 128 f32 or 256 bf16 logits.  Measured at T=16384, us per
-// call, 64 lanes -> 16: bf16 E=64 7.3 -> 6.2, E=256 8.5 -> 6.1 (gradient 11.4 -> 9.4);
-// f32 E=64 7.8 -> 6.1, E=128 8.5 -> 6.6 (gradient 9.3 -> 7.2), but E=256 10.5 -> 11.2
-// (gradient 12.2 -> 13.5).
+// 16 lanes per token up to 64 logits; up to 128 f32 or 256 bf16 ones where there are
+// tokens enough to fill the chip at four a wave, since the lists of 8 or 16 logits a
+// lane make the single token's chain longer.  Measured, us on the GPU, 64 lanes -> 16:
+//   T=16384 (a call)  bf16 E=64 7.3 -> 6.2, E=256 8.5 -> 6.1, its gradient 11.4 -> 9.4;
+//                     f32 E=64 7.8 -> 6.1, E=128 8.5 -> 6.6, its gradient 9.3 -> 7.2;
+//                     but f32 E=256 10.5 -> 11.2, its gradient 12.2 -> 13.5
+//   T=8192            bf16 E=256 6.6 -> 5.5; f32 E=128 6.4 -> 6.1, E=16 5.7 -> 3.4
+//   T=4096            bf16 E=256 4.8 -> 5.1; f32 E=128 4.8 -> 6.0, E=16 4.2 -> 3.4
+//   T=512             bf16 E=256 4.0 -> 4.8; f32 E=128 4.0 -> 6.9, E=16 3.6 -> 3.3
+constexpr int64_t kFewTokens = 4096;
 template <bool F32>
 void by_e(const GateArgs& a, bool backward, hipStream_t s) {
+    const bool few = a.T <= kFewTokens;
     if (a.E <= 16) return go<16, 1, F32>(a, backward, s);
     if (a.E <= 32) return go<16, 2, F32>(a, backward, s);
     if (a.E <= 64) return go<16, 4, F32>(a, backward, s);
-    if (a.E <= 128) return go<16, 8, F32>(a, backward, s);
-    if (a.E <= 256) return F32 ? go<64, 4, true>(a, backward, s) : go<16, 16, false>(a, backward, s);
+    if (a.E <= 128) return few ? go<64, 2, F32>(a, backward, s) : go<16, 8, F32>(a, backward, s);
+    if (a.E <= 256)
+        return F32 || few ? go<64, 4, F32>(a, backward, s) : go<16, 16, false>(a, backward, s);
     if (a.E <= 512) return go<64, 8, F32>(a, backward, s);
     go<64, 16, F32>(a, backward, s);
 }

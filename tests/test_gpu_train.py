@@ -104,7 +104,7 @@ def _logits(g, T, E, dt, kind):
 
 GATE_SHAPES = [(1, 1, 1), (1, 8, 8), (3, 16, 16), (5, 63, 5), (7, 64, 6), (130, 65, 4), (33, 128, 8),
                (257, 200, 8), (64, 256, 8), (19, 257, 3), (9, 511, 16), (6, 512, 10), (5, 1000, 16),
-               (31, 1024, 8)]
+               (31, 1024, 8), (4097, 100, 8), (4101, 256, 4), (4098, 192, 16)]
 
 
 @pytest.mark.parametrize("kind", ["normal", "ties", "masked", "wide"])

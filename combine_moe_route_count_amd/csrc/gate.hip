@@ -382,16 +382,25 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateArgs a,
         const float dot = Group<G>::sum(d);
         const float mine = a.renorm ? d - p * dot : d;
         float g[V];
+        const float all = dot / total;
 #pragma unroll
-        for (int i = 0; i < V; ++i) g[i] = a.renorm ? 0.0f : -((v[i] / total) * dot);
+        for (int i = 0; i < V; ++i) g[i] = a.renorm ? 0.0f : -(v[i] * all);
         // in order of k, so an expert named twice gets both in a fixed order
         for (int k = 0; k < a.K; ++k) {
             const int jk = Group<G>::share(j, k);
             const float x = Group<G>::share(mine, k);
-            const int at = jk - gl * V;    // no place of this lane where jk is -1
+            if constexpr (G == kWave) {    // one token: jk is the same in every lane
+                if (jk < 0) continue;
+                const float here = gl == jk / V ? x : 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (jk >= 0 && at == i) g[i] += x;
+                for (int i = 0; i < V; ++i)
+                    if (jk % V == i) g[i] += here;
+            } else {
+                const int at = jk - gl * V;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (jk >= 0 && at == i) g[i] += x;
+            }
         }
         if (live) store_logits<V, F32>(a.dlogits, t, a.E, gl, vec, g);
     }

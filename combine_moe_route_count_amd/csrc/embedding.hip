@@ -64,26 +64,12 @@ __global__ __launch_bounds__(lookup_threads(OF32)) void embedding_kernel(Embeddi
     constexpr int EL = OF32 ? 4 : 8;
     const int units = (int)(a.H / EL);
     const int64_t items = a.N * nch;
-    // the last item counts the ids outside [0,V)
-    for (int64_t wi = blockIdx.x; wi < items + (a.stats ? 1 : 0); wi += gridDim.x) {
-        if (wi == items) {
-            __shared__ int32_t bad;
-            if (threadIdx.x == 0) bad = 0;
-            __syncthreads();
-            int32_t mine = 0;
-            for (int64_t n = threadIdx.x; n < a.N; n += blockDim.x) {
-                const int64_t id = token_id(a.ids, a.id_bytes, n);
-                mine += id < -1 || id >= a.V;
-            }
-            if (mine) atomicAdd(&bad, mine);
-            __syncthreads();
-            if (threadIdx.x == 0) a.stats[0] = bad;
-            continue;
-        }
+    for (int64_t wi = blockIdx.x; wi < items; wi += gridDim.x) {
         const int64_t n = wi / nch;
         const int c = (int)(wi - n * nch);
         const int64_t id = token_id(a.ids, a.id_bytes, n);
         const bool some = id >= 0 && id < a.V;
+        if (a.stats && !some && id != -1 && c == 0 && threadIdx.x == 0) atomicAdd(a.stats, 1);
         const int u0 = c * kLookupUnits * (int)blockDim.x + (int)threadIdx.x;
         FloatUnit<TF32, EL> x[kLookupUnits];
 #pragma unroll
@@ -108,13 +94,18 @@ __global__ __launch_bounds__(lookup_threads(OF32)) void embedding_kernel(Embeddi
     }
 }
 
+// The count of ids outside [0,V) starts at 0 in a launch of its own: the lookup then
+// adds to it for such ids only.
+__global__ void clear_count_kernel(int32_t* stats) { *stats = 0; }
+
 template <bool TF32, bool OF32>
 void embedding_go(const EmbeddingArgs& a, hipStream_t s) {
     const int64_t units = a.H / (OF32 ? 4 : 8);
     const int threads = row_threads((units + kLookupUnits - 1) / kLookupUnits, lookup_threads(OF32));
     const int nch = (int)((units + threads * kLookupUnits - 1) / (threads * kLookupUnits));
-    embedding_kernel<TF32, OF32>
-        <<<capped_grid(a.N * nch + (a.stats ? 1 : 0)), dim3(threads), 0, s>>>(a, nch);
+    if (a.stats) clear_count_kernel<<<dim3(1), dim3(1), 0, s>>>(a.stats);
+    if (a.N > 0)
+        embedding_kernel<TF32, OF32><<<capped_grid(a.N * nch), dim3(threads), 0, s>>>(a, nch);
 }
 
 // ---------------------------------------------------------------------------

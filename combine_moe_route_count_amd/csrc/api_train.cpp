@@ -170,20 +170,26 @@ MOE_API int moe_combine_backward(const void* dout, moe_dtype dout_dt, const floa
         MOE_TRY(check_float(dy_dt, "dy"));
         MOE_TRY(check_rows_ptr(dy, y_rows, "dy"));
         MOE_TRY(check_elems(w, T, 4, "w"));
-        const int64_t b = y_rows * H * float_bytes(dy_dt);
-        MOE_TRY(check_apart(dy, b, "dy", dout, dout_bytes, "dout"));
-        MOE_TRY(check_apart(dy, b, "dy", y, y_bytes, "y"));
-        MOE_TRY(check_apart(dy, b, "dy", tok_map, T * K * 8, "tok_map"));
-        MOE_TRY(check_apart(dy, b, "dy", w, T * K * 4, "w"));
-        MOE_TRY(check_apart(dy, b, "dy", dw, T * K * 4, "dw"));
     }
-    if (dw) {
-        const int64_t b = T * K * 4;
-        MOE_TRY(check_apart(dw, b, "dw", dout, dout_bytes, "dout"));
-        MOE_TRY(check_apart(dw, b, "dw", y, y_bytes, "y"));
-        MOE_TRY(check_apart(dw, b, "dw", tok_map, T * K * 8, "tok_map"));
-        if (dy) MOE_TRY(check_apart(dw, b, "dw", w, b, "w"));
+    // what the call reads; y and its scales for dw only, w and the segments for dy only
+    const struct {
+        const void* p;
+        int64_t bytes;
+        const char* name;
+    } in[] = {{dout, dout_bytes, "dout"},
+              {dout_weights, dw ? T * 4 : 0, "dout_weights"},
+              {y, y_bytes, "y"},
+              {y_scales, dw ? y_rows * (H / 128) * 4 : 0, "y_scales"},
+              {tok_map, T * K * 8, "tok_map"},
+              {w, dy ? T * K * 4 : 0, "w"},
+              {packed_cnt, dy ? (int64_t)E * 4 : 0, "packed_cnt"},
+              {packed_off, dy ? ((int64_t)E + 1) * 4 : 0, "packed_off"}};
+    const int64_t dy_bytes = y_rows * H * float_bytes(dy_dt);
+    for (const auto& i : in) {
+        MOE_TRY(check_apart(dy, dy_bytes, "dy", i.p, i.bytes, i.name));
+        MOE_TRY(check_apart(dw, T * K * 4, "dw", i.p, i.bytes, i.name));
     }
+    MOE_TRY(check_apart(dy, dy_bytes, "dy", dw, T * K * 4, "dw"));
     moe::CombineGradArgs a{};
     a.dout = dout;
     a.dout_f32 = dout_dt == MOE_F32;

@@ -108,8 +108,9 @@ int moe_embedding(const void* table, moe_dtype table_dt, int64_t V, int64_t H, c
 
 /* Bytes of device workspace that moe_embedding_backward needs for these sizes (0
  * for sizes outside the limits).  It needs no initialisation, may be reused by
- * consecutive calls on one stream, also from a captured graph, and must not be
- * shared by calls that may run at the same time. */
+ * consecutive calls on one stream, also from a captured graph.  Calls that may run
+ * at the same time, or that several host threads enqueue at the same time, need
+ * workspaces of their own. */
 size_t moe_embedding_workspace_size(int64_t N, int64_t V, int64_t H);
 
 /* Gradient of the embedding lookup with respect to the table:

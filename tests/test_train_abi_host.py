@@ -88,7 +88,9 @@ res["combine_backward"] = {
     "pc_odd": comb(pc=B["pc"] + 2), "dy_on_y": comb(dy=B["y"]), "dy_on_dout": comb(dy=B["dout"]),
     "dy_on_w": comb(dy=B["w"] & ~15), "dy_on_tm": comb(dy=B["tm"]), "dw_on_y": comb(dw=B["y"] + 64),
     "dw_on_dy": comb(dw=B["dy"] + 64), "dw_on_w": comb(dw=B["w"]), "dw_on_tm": comb(dw=B["tm"]),
-    "dw_on_dout": comb(dw=B["dout"]),
+    "dw_on_dout": comb(dw=B["dout"]), "dw_on_dow": comb(dw=B["dow"]), "dy_on_dow": comb(dy=B["dow"]),
+    "dw_on_scales": comb(ydt=2, ys=B["ys"], dw=B["ys"] + 8), "dy_on_scales": comb(ydt=3, ys=B["ys"], dy=B["ys"]),
+    "dy_on_pc": comb(dy=B["pc"]), "dy_on_po": comb(dy=B["po"]), "dw_on_po": comb(dw=B["po"] + 32),
 }
 disp = case(lib.moe_dispatch_backward, "dp ddt rows H tm T K res dx dxdt".split(),
             dict(dp=B["dp"], ddt=0, rows=10, H=64, tm=B["tm"], T=5, K=2, res=B["res"], dx=B["dx"], dxdt=0))

@@ -13,15 +13,19 @@
 // occurs once or in half of all positions.
 //
 // The sort: up to kSmallSort positions are ranked by counting, one launch.  More are
-// radix sorted; a digit (at most 9 bits) is the key of the one-launch routing
-// (route_fused.hip), so a pass is its stable slots and the move of (id, position).
+// radix sorted by digits of at most 9 bits, with the routing's stable ranks inside
+// tiles of 1024 (route_device.hpp): a pass ranks the tiles, and then moves (id,
+// position).  Up to kOwnScanTiles tiles, each moving workgroup sums the tiles' counts
+// for itself; more tiles go through the one-launch routing (route_fused.hip), whose
+// last workgroup scans them.
 //
 // What bounds it: one read of dout's rows and one write of the table, most of it zeros
 // for a large vocabulary.  65536 tokens of 4096 (bf16, Zipf) into 131072 f32 rows, 2.66
-// GB: 474 us = 5.6 TB/s, of it zeros 260 us (7.0 TB/s), windows 161 (5.2 TB/s), sort 37
+// GB: 469 us = 5.7 TB/s, of it zeros 260 us (7.0 TB/s), windows 161 (5.2 TB/s), sort 23
 // and join 15.
 #include "train_device.hpp"
 #include "internal.hpp"
+#include "route_device.hpp"
 
 namespace moe {
 
@@ -30,13 +34,17 @@ namespace {
 constexpr int kEmbThreads = 256;
 constexpr int kSmallSort = 4096;   // positions
 
-// Most bits of a digit: 9 (512 keys, the most that the one-launch routing takes), and
-// fewer for long inputs, so that its scan keeps all of its tiles x keys counts in
-// registers.
-constexpr int64_t kDigitCounts = 16384;
+// Bits of a digit: at most 9 (512 keys).  Fewer for long inputs: own scans read tiles x
+// tiles x keys counts in all, which stay under 2^24; the one-launch routing keeps its
+// tiles x keys counts in registers up to 2^14.  Own scans against the routing, the whole
+// gradient: 10136 tokens of 80 35.0 and 39.7 us, 65536 of 64 48.9 and 63.2, 131072 of 256
+// 65.5 and 82.7, 262144 of 256 115 and 131.
+constexpr int64_t kOwnScanTiles = 256;
 inline int digit_bits(int64_t tiles) {
     int bits = 9;
-    while (bits > 4 && (tiles << bits) > kDigitCounts) --bits;
+    while (bits > 4 && (tiles <= kOwnScanTiles ? (tiles * tiles) << bits > (1 << 24)
+                                               : tiles << bits > (1 << 14)))
+        --bits;
     return bits;
 }
 
@@ -133,10 +141,9 @@ ZeroRows zero_layout(int64_t V, int64_t H, bool f32) {
     return z;
 }
 
-// The lane's row and unit of block b; false if it has none.
-__device__ __forceinline__ bool zero_place(const ZeroRows& z, int64_t b, int64_t V, int64_t& v,
-                                           int& u) {
-    const int tid = threadIdx.x;
+// Row and unit of thread tid of block b; false if it has none.
+__device__ __forceinline__ bool zero_place(const ZeroRows& z, int64_t b, int tid, int64_t V,
+                                           int64_t& v, int& u) {
     if (z.chunks > 1 || z.rows == 1) {
         v = b / z.chunks;
         u = (int)(b - v * z.chunks) * kEmbThreads + tid;
@@ -157,13 +164,14 @@ __device__ __forceinline__ void zero_store(void* table, int64_t H, int64_t v, in
     store_unit<OF32, true>(table, v * H + (int64_t)u * EL, z);
 }
 
-struct MoveArgs {              // one radix pass's move
+struct MoveArgs {              // one radix pass
     DigitSource d;
     int64_t N;
-    const int32_t* local_rank;
-    const int32_t* tile_base;  // [tiles][NK]
-    const int32_t* off;        // [NK+1]
-    int NK;
+    int32_t* local_rank;
+    int32_t* tile_cnt;         // [tiles][NK] counts; after the one-launch routing, bases
+    int32_t* tile_flags;
+    int32_t* off;              // [NK+1]
+    int tiles, NK, nbits;
     const int32_t* in_pos;     // null: the position is the entry's own number
     int32_t* out_id;
     int32_t* out_pos;
@@ -177,30 +185,101 @@ struct MoveArgs {              // one radix pass's move
     ZeroRows zero;
 };
 
-__global__ __launch_bounds__(kEmbThreads) void move_kernel(MoveArgs a) {
-    for (int64_t b = (int64_t)blockIdx.x - a.move_blocks; a.dtable && b < a.zero.blocks;
-         b += gridDim.x) {
-        int64_t v;
-        int u;
-        if (b < 0 || !zero_place(a.zero, b, a.V, v, u)) continue;
-        if (a.dtable_f32) zero_store<true>(a.dtable, a.H, v, u);
-        else zero_store<false>(a.dtable, a.H, v, u);
+constexpr int kSortThreads = kTile;   // a tile per workgroup, an entry per thread
+constexpr int kSortWaves = kSortThreads / kWave;
+constexpr int64_t kMaxSortGrid = (int64_t)1 << 20;   // moving, and as many zeroing
+
+__global__ __launch_bounds__(kSortThreads) void digit_rank_kernel(MoveArgs a) {
+    extern __shared__ int32_t run_all[];   // [kSortWaves][NK]
+    rank_tile<kSortWaves, 1>(DigitKeys{a.d}, a.N, a.NK, a.nbits, (int64_t)blockIdx.x, run_all,
+                             a.local_rank, a.tile_cnt, a.tile_flags);
+}
+
+// Zeroing and clearing beside a move; false if this workgroup moves nothing.
+__device__ __forceinline__ bool beside_move(const MoveArgs& a) {
+    constexpr int kParts = kSortThreads / kEmbThreads;
+    const int part = threadIdx.x / kEmbThreads, tid = threadIdx.x % kEmbThreads;
+    if (blockIdx.x >= a.move_blocks) {
+        for (int64_t b = ((int64_t)blockIdx.x - a.move_blocks) * kParts + part; b < a.zero.blocks;
+             b += ((int64_t)gridDim.x - a.move_blocks) * kParts) {
+            int64_t v;
+            int u;
+            if (!zero_place(a.zero, b, tid, a.V, v, u)) continue;
+            if (a.dtable_f32) zero_store<true>(a.dtable, a.H, v, u);
+            else zero_store<false>(a.dtable, a.H, v, u);
+        }
+        return false;
     }
-    if (blockIdx.x >= a.move_blocks) return;
-    const int64_t step = a.move_blocks * kEmbThreads;
-    const int64_t first = (int64_t)blockIdx.x * kEmbThreads + threadIdx.x;
-    if (a.clear)
-        for (int64_t v = first; v < a.V; v += step) a.clear[v] = 0;
-    for (int64_t f = first; f < a.N; f += step) {
+    if (a.clear) {
+        const int64_t step = a.move_blocks * kSortThreads;
+        for (int64_t v = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; v < a.V; v += step)
+            a.clear[v] = 0;
+    }
+    return true;
+}
+
+__device__ __forceinline__ int32_t entry_id(const DigitSource& d, int64_t f) {
+    return d.total ? ((const int32_t*)d.ids)[f] : (int32_t)token_id(d.ids, d.id_bytes, f);
+}
+
+__device__ __forceinline__ void move_entry(const MoveArgs& a, int64_t f, int32_t id, int64_t to) {
+    a.out_id[to] = id;
+    a.out_pos[to] = a.in_pos ? a.in_pos[f] : (int32_t)f;
+    if (a.present) a.present[id] = 1;
+}
+
+// Move of one tile per workgroup behind its own scan: thread (key, part) sums the counts
+// of a stretch of tiles, in all and before this tile.
+__global__ __launch_bounds__(kSortThreads) void scan_move_kernel(MoveArgs a) {
+    __shared__ int32_t before_lds[kSortThreads], total_lds[kSortThreads];
+    __shared__ int32_t wave_sums[kScanThreads / kWave];
+    if (!beside_move(a)) return;
+    const int tid = threadIdx.x;
+    const int tile = blockIdx.x;
+    const int64_t f = (int64_t)tile * kTile + tid;
+    const int32_t lr = f < a.N ? a.local_rank[f] : -1;
+    const int32_t id = lr >= 0 ? entry_id(a.d, f) : 0;
+    const int parts = kSortThreads / a.NK, per = (a.tiles + parts - 1) / parts;
+    const int key = tid % a.NK, part = tid / a.NK;
+    const int t0 = part * per, t1 = t0 + per < a.tiles ? t0 + per : a.tiles;
+    int32_t before = 0, total = 0;
+#pragma unroll 8
+    for (int t = t0; t < t1; ++t) {
+        const int32_t c = a.tile_cnt[(int64_t)t * a.NK + key];
+        total += c;
+        before += t < tile ? c : 0;
+    }
+    before_lds[tid] = before;
+    total_lds[tid] = total;
+    __syncthreads();
+    if (tid < a.NK)
+        for (int p = 1; p < parts; ++p) {
+            before += before_lds[p * a.NK + tid];
+            total += total_lds[p * a.NK + tid];
+        }
+    const int32_t first = block_exclusive_scan(tid < a.NK ? total : 0, wave_sums);
+    if (tid < a.NK) {
+        before_lds[tid] = first + before;     // read by nobody else before the barrier
+        if (tile == 0) {
+            a.off[tid] = first;
+            if (tid == a.NK - 1) a.off[a.NK] = first + total;
+        }
+    }
+    __syncthreads();
+    if (lr >= 0)
+        move_entry(a, f, id, (int64_t)before_lds[(id >> a.d.shift) & a.d.mask] + lr);
+}
+
+// Move behind the one-launch routing, which left the tiles' bases and the offsets.
+__global__ __launch_bounds__(kSortThreads) void move_kernel(MoveArgs a) {
+    if (!beside_move(a)) return;
+    const int64_t step = a.move_blocks * kSortThreads;
+    for (int64_t f = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; f < a.N; f += step) {
         const int32_t lr = a.local_rank[f];
         if (lr < 0) continue;
-        const int32_t id = a.d.total ? ((const int32_t*)a.d.ids)[f]
-                                     : (int32_t)token_id(a.d.ids, a.d.id_bytes, f);
+        const int32_t id = entry_id(a.d, f);
         const int key = (id >> a.d.shift) & a.d.mask;
-        const int64_t to = (int64_t)a.off[key] + a.tile_base[(f / kTile) * a.NK + key] + lr;
-        a.out_id[to] = id;
-        a.out_pos[to] = a.in_pos ? a.in_pos[f] : (int32_t)f;
-        if (a.present) a.present[id] = 1;
+        move_entry(a, f, id, (int64_t)a.off[key] + a.tile_cnt[(f / kTile) * a.NK + key] + lr);
     }
 }
 
@@ -234,7 +313,7 @@ __global__ __launch_bounds__(kEmbThreads) void small_sort_kernel(SmallSortArgs a
         if (b >= a.sort_blocks) {
             int64_t v;
             int u;
-            if (zero_place(a.zero, b - a.sort_blocks, a.V, v, u))
+            if (zero_place(a.zero, b - a.sort_blocks, tid, a.V, v, u))
                 zero_store<OF32>(a.dtable, a.H, v, u);
             continue;
         }
@@ -298,7 +377,7 @@ __global__ __launch_bounds__(kEmbThreads) void zero_rows_kernel(void* table, int
     for (int64_t b = blockIdx.x; b < z.blocks; b += gridDim.x) {
         int64_t v;
         int u;
-        if (!zero_place(z, b, V, v, u)) continue;
+        if (!zero_place(z, b, threadIdx.x, V, v, u)) continue;
         const bool some = present ? present[v] != 0 : off[v + 1] != off[v];
         if (!some) zero_store<OF32>(table, H, v, u);
     }
@@ -391,12 +470,16 @@ __global__ __launch_bounds__(kEmbThreads) void windows_kernel(SumArgs a) {
 }
 
 // Runs that cross windows: workgroup (window in which the run begins, chunk) adds the
-// parts in order.  Letting the waves share the parts of a long run (sums of stretches
-// through LDS) was slower everywhere, its registers and LDS cost the short ones more:
-// 65536 tokens 496 -> 525 us, 8192 tokens over 200 rows 37 -> 42.
+// parts in order.  Where a row leaves threads over, they share the parts: `share`
+// stretches of consecutive ones, whose sums are added in order (10136 tokens of 80:
+// 34.9 us for the whole gradient with one stretch, 26.6 with 12; 131072 of 256 65.6 and
+// 56.5 with 4).  For wide rows the same
+// through several units per thread was slower, its registers and LDS cost the short
+// runs more: 65536 tokens of 4096 496 -> 525 us, 8192 tokens over 200 rows 37 -> 42.
 template <bool OF32>
-__global__ __launch_bounds__(kEmbThreads) void join_kernel(SumArgs a, int nch) {
+__global__ __launch_bounds__(kEmbThreads) void join_kernel(SumArgs a, int nch, int share) {
     constexpr int EL = 4;
+    __shared__ float stretch[kEmbThreads][EL];
     const int lane = threadIdx.x % kWave;
     const int units = (int)(a.g.H / EL);
     const int64_t m = *a.total;
@@ -419,41 +502,62 @@ __global__ __launch_bounds__(kEmbThreads) void join_kernel(SumArgs a, int nch) {
             more += __builtin_ctzll(no);
             break;
         }
-        const int u = (int)(b - w * nch) * (int)blockDim.x + (int)threadIdx.x;
-        if (u >= units) continue;
+        const int s = share > 1 ? (int)threadIdx.x / units : 0;   // this thread's stretch
+        const int u = share > 1 ? (int)threadIdx.x - s * units
+                                : (int)(b - w * nch) * (int)blockDim.x + (int)threadIdx.x;
+        const bool mine = u < units && s < share;
         const int64_t col = (int64_t)u * EL;
+        const int64_t per = (more + share - 1) / share;
+        const int64_t from = s * per, to = from + per < more ? from + per : more;
         float acc[EL];
-        FloatUnit<true, EL> x0;
-        x0.load(a.partial, (2 * w + 1) * a.g.H + col);
+#pragma unroll
+        for (int j = 0; j < EL; ++j) acc[j] = 0.0f;
         FloatUnit<OF32, EL> base;
-        if (a.g.accumulate) base.load(a.g.dtable, (int64_t)v * a.g.H + col);
-        x0.get(acc);
-        for (int64_t i = 0; i < more; i += kBatch) {
+        if (mine && s == 0) {
+            FloatUnit<true, EL> x0;
+            x0.load(a.partial, (2 * w + 1) * a.g.H + col);
+            if (a.g.accumulate) base.load(a.g.dtable, (int64_t)v * a.g.H + col);
+            x0.get(acc);
+        }
+        for (int64_t i = from; mine && i < to; i += kBatch) {
             FloatUnit<true, EL> x[kBatch];
 #pragma unroll
             for (int q = 0; q < kBatch; ++q)
-                if (i + q < more) x[q].load(a.partial, 2 * (w + 1 + i + q) * a.g.H + col);
+                if (i + q < to) x[q].load(a.partial, 2 * (w + 1 + i + q) * a.g.H + col);
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
-                if (i + q >= more) continue;
+                if (i + q >= to) continue;
                 float p[EL];
                 x[q].get(p);
 #pragma unroll
                 for (int j = 0; j < EL; ++j) acc[j] += p[j];
             }
         }
-        put_row<OF32, EL>(a, v, col, acc, a.g.accumulate ? &base : nullptr);
+        if (share > 1) {
+            __syncthreads();   // the previous run's stretches are read
+#pragma unroll
+            for (int j = 0; j < EL; ++j) stretch[threadIdx.x][j] = acc[j];
+            __syncthreads();
+            if (mine && s == 0)
+                for (int i = 1; i < share; ++i)
+#pragma unroll
+                    for (int j = 0; j < EL; ++j) acc[j] += stretch[i * units + u][j];
+        }
+        if (mine && s == 0)
+            put_row<OF32, EL>(a, v, col, acc, a.g.accumulate ? &base : nullptr);
     }
 }
 
-// Positions per window: 64 (one wave's lanes), fewer while there would be less than
-// kWantWaves waves of 512 elements.  8192 tokens of 1024 over 100 rows: 29.6 us with
-// 1024, 37.4 with 2048 or 4096; of 4096 over 200 rows 37.1, 34.1, 38.4; 65536 tokens
-// of 264 92, 93, 106.
-constexpr int64_t kWantWaves = 1024;
+// Positions per window: 64 (one wave's lanes), fewer while there would be less than so
+// many waves of 512 elements: shorter windows make more workgroups and longer joins,
+// and narrow rows share those.  Measured with 512 / 1024 / 2048 / 4096, us: 65536 tokens
+// of 64 - / 44.4 / 39.5 / 39.0, of 264 - / 75.0 / 72.8 / 77.3; 8192 tokens of 1024 over
+// 100 rows 24.0 / 26.2 / 33.8 / -, of 4096 over 200 rows 32.6 / 32.5 / 30.3 / -; 4096
+// of 1024 over 100 rows 23.0 / 27.0 / 26.9 / -.
 inline int window_of(int64_t N, int64_t H) {
+    const int64_t waves = H <= 512 ? 2048 : 512;
     int w = kWave;
-    while (w > 8 && (N + w - 1) / w * ((H + 511) / 512) < kWantWaves) w /= 2;
+    while (w > 8 && (N + w - 1) / w * ((H + 511) / 512) < waves) w /= 2;
     return w;
 }
 
@@ -520,11 +624,6 @@ P* at(void* ws, size_t off) {
     return (P*)((char*)ws + off);
 }
 
-inline int64_t flat_blocks(int64_t n) {
-    const int64_t b = (n + kEmbThreads - 1) / kEmbThreads;
-    return b < kMaxGrid ? b : kMaxGrid;
-}
-
 inline int chunks(int64_t units, int threads) { return (int)((units + threads - 1) / threads); }
 
 template <bool OF32>
@@ -547,68 +646,76 @@ hipError_t small_sort(const EmbeddingGradArgs& g, const SumArgs& a, hipStream_t 
     return hipGetLastError();
 }
 
-// Sorts by one digit after the other; returns which of the two buffers holds the result.
+// Ranks of one digit by the one-launch routing, scanned by its last workgroup.
+hipError_t route_digit(const MoveArgs& m, uint64_t* ticket, hipStream_t s) {
+    RouteFusedArgs fa{};
+    fa.kind = KeyKind::Digits;
+    fa.digits = m.d;
+    fa.N = m.N;
+    fa.nbits = m.nbits;
+    fa.local_rank = m.local_rank;
+    fa.ticket = ticket;
+    fa.scan.tile_cnt = m.tile_cnt;
+    fa.scan.tile_flags = m.tile_flags;
+    fa.scan.tiles = m.tiles;
+    fa.scan.NK = m.NK;
+    fa.scan.rows_limit = INT64_MAX;
+    fa.scan.off_ws = m.off;
+    fa.scan.mode = StatsMode::Plain;
+    return launch_route_fused(fa, s);
+}
+
+// Sorts by one digit after the other; cur: which of the two buffers holds the result.
 hipError_t radix_sort(const EmbeddingGradArgs& g, const GradWs& w, int& cur, hipStream_t s) {
     void* ws = g.ws;
-    const int NK = 1 << w.bits;
+    const bool own_scan = w.tiles <= kOwnScanTiles;
+    MoveArgs m{};
+    m.N = g.N;
+    m.V = g.V;
+    m.H = g.H;
+    m.local_rank = at<int32_t>(ws, w.local_rank);
+    m.tile_cnt = at<int32_t>(ws, w.tile_cnt);
+    m.tile_flags = at<int32_t>(ws, w.tile_flags);
+    m.tiles = (int)w.tiles;
+    m.NK = 1 << w.bits;
+    m.nbits = w.bits;
+    m.d.mask = m.NK - 1;
     cur = 0;
     for (int p = 0; p < w.passes; ++p) {
-        DigitSource d{};
-        d.shift = p * w.bits;
-        d.mask = NK - 1;
-        if (p == 0) {
-            d.ids = g.ids;
-            d.id_bytes = g.id_bytes;
-            d.V = g.V;
+        const bool first = p == 0, last = p == w.passes - 1;
+        m.d.shift = p * w.bits;
+        m.d.ids = first ? g.ids : at<int32_t>(ws, w.id[cur]);
+        m.d.id_bytes = first ? g.id_bytes : 4;
+        m.d.V = g.V;
+        m.d.total = first ? nullptr : at<int32_t>(ws, w.off0) + m.NK;
+        m.off = at<int32_t>(ws, first ? w.off0 : w.off);
+        if (own_scan) {
+            digit_rank_kernel<<<dim3((unsigned)w.tiles), dim3(kSortThreads),
+                                sizeof(int32_t) * kSortWaves * m.NK, s>>>(m);
         } else {
-            d.ids = at<int32_t>(ws, w.id[cur]);
-            d.total = at<int32_t>(ws, w.off0) + NK;
+            const hipError_t e = route_digit(m, at<uint64_t>(ws, w.ticket), s);
+            if (e != hipSuccess) return e;
         }
-        int32_t* off = at<int32_t>(ws, p == 0 ? w.off0 : w.off);
-        RouteFusedArgs fa{};
-        fa.kind = KeyKind::Digits;
-        fa.digits = d;
-        fa.N = g.N;
-        fa.nbits = w.bits;
-        fa.local_rank = at<int32_t>(ws, w.local_rank);
-        fa.ticket = at<uint64_t>(ws, w.ticket);
-        fa.scan.tile_cnt = at<int32_t>(ws, w.tile_cnt);
-        fa.scan.tile_flags = at<int32_t>(ws, w.tile_flags);
-        fa.scan.tiles = (int)w.tiles;
-        fa.scan.NK = NK;
-        fa.scan.rows_limit = INT64_MAX;
-        fa.scan.off_ws = off;
-        fa.scan.mode = StatsMode::Plain;
-        const hipError_t e = launch_route_fused(fa, s);
-        if (e != hipSuccess) return e;
-        MoveArgs m{};
-        m.d = d;
-        m.N = g.N;
-        m.local_rank = fa.local_rank;
-        m.tile_base = fa.scan.tile_cnt;
-        m.off = off;
-        m.NK = NK;
-        const int next = p == 0 ? 0 : 1 - cur;
-        m.in_pos = p == 0 ? nullptr : at<int32_t>(ws, w.pos[cur]);
+        const int next = first ? 0 : 1 - cur;
+        m.in_pos = first ? nullptr : at<int32_t>(ws, w.pos[cur]);
         m.out_id = at<int32_t>(ws, w.id[next]);
         m.out_pos = at<int32_t>(ws, w.pos[next]);
-        m.V = g.V;
-        m.H = g.H;
-        if (g.accumulate) {
-            // nothing is zeroed
-        } else if (w.zero_early) {
-            if (p == 0) {
-                m.dtable = g.dtable;
-                m.dtable_f32 = g.dtable_f32;
-                m.zero = zero_layout(g.V, g.H, g.dtable_f32);
-            }
-        } else if (w.passes > 1) {
-            if (p == 0) m.clear = at<uint8_t>(ws, w.present);
-            if (p == w.passes - 1) m.present = at<uint8_t>(ws, w.present);
+        const bool flags = w.passes > 1 && !w.zero_early && !g.accumulate;
+        m.clear = flags && first ? at<uint8_t>(ws, w.present) : nullptr;
+        m.present = flags && last ? at<uint8_t>(ws, w.present) : nullptr;
+        m.move_blocks = w.tiles < kMaxSortGrid ? w.tiles : kMaxSortGrid;
+        int64_t zero_blocks = 0;
+        if (first && w.zero_early && !g.accumulate) {
+            m.dtable = g.dtable;
+            m.dtable_f32 = g.dtable_f32;
+            m.zero = zero_layout(g.V, g.H, g.dtable_f32);
+            constexpr int kParts = kSortThreads / kEmbThreads;
+            zero_blocks = (m.zero.blocks + kParts - 1) / kParts;
+            if (zero_blocks > kMaxSortGrid) zero_blocks = kMaxSortGrid;
         }
-        m.move_blocks = flat_blocks(m.clear && g.V > g.N ? g.V : g.N);
-        move_kernel<<<capped_grid(m.move_blocks + (m.dtable ? m.zero.blocks : 0)),
-                      dim3(kEmbThreads), 0, s>>>(m);
+        const dim3 grid((unsigned)(m.move_blocks + zero_blocks));
+        if (own_scan) scan_move_kernel<<<grid, dim3(kSortThreads), 0, s>>>(m);
+        else move_kernel<<<grid, dim3(kSortThreads), 0, s>>>(m);
         cur = next;
     }
     return hipGetLastError();
@@ -647,9 +754,11 @@ hipError_t grad_go(const EmbeddingGradArgs& g, hipStream_t s) {
     if (g.accumulate) windows_kernel<DF32, OF32, true><<<grid, dim3(threads), 0, s>>>(a);
     else windows_kernel<DF32, OF32, false><<<grid, dim3(threads), 0, s>>>(a);
     if (a.windows > 1) {
-        const int jt = row_threads(g.H / 4, kEmbThreads);
-        const int jch = chunks(g.H / 4, jt);
-        join_kernel<OF32><<<capped_grid(a.windows * jch), dim3(jt), 0, s>>>(a, jch);
+        const int64_t ju = g.H / 4;
+        const int share = ju < kEmbThreads ? (int)(kEmbThreads / ju) : 1;
+        const int jt = share > 1 ? kEmbThreads : row_threads(ju, kEmbThreads);
+        const int jch = chunks(ju, jt);
+        join_kernel<OF32><<<capped_grid(a.windows * jch), dim3(jt), 0, s>>>(a, jch, share);
     }
     return hipGetLastError();
 }

@@ -288,8 +288,9 @@ __global__ __launch_bounds__(kSortThreads) void move_kernel(MoveArgs a) {
 // the remaining workgroups zero the whole table meanwhile (zero_blocks, none when
 // accumulating), so the sums need not know which rows to clear.  The whole gradient
 // with 777 tokens took 18.5, 14.9 and 14.7 us at 4, 16 and 32 threads per position.
-// At 4096 tokens it took 142 us by counting and 150 by digits (50000 rows of 4096
-// f32), 26.5 and 27.1 (100 rows); at 8192 tokens 180 against 159, and 41 against 29.
+// By counting and by digits: 3000 tokens into 3000 rows of 256 16.9 and 22.4 us, 4096
+// into 50000 rows of 2048 f32 78.6 and 87.5, but into 512 rows of 64 (one digit) 18.2
+// and 16.2; 8192 into 50000 rows of 4096 180 and 159.
 constexpr int kSortShare = 32;
 constexpr int kSortPositions = kEmbThreads / kSortShare;
 

@@ -514,7 +514,7 @@ GRAD = [(1, 1, 8, "uniform"), (0, 9, 16, "uniform"), (1, 600, 7168, "uniform"), 
         (4099, 1000, 136, "same"), (5000, 262145, 8, "zipf"), (9000, 50, 64, "runs"), (20000, 3000, 48, "zipf"),
         (4096, 700, 64, "zipf"), (4097, 512, 8, "padded"), (4100, 500, 33016, "padded"),
         (5000, 6001, 4104, "zipf"), (4608, 9, 24, "same"), (70000, 200, 8, "zipf"),
-        (300000, 5000, 8, "runs")]
+        (300000, 5000, 8, "runs"), (262144, 3000, 8, "zipf"), (262145, 700, 16, "padded")]
 
 
 def _grad_ref(dout, ids, V, scale):
@@ -759,6 +759,25 @@ def test_rows_past_four_gib():
     moe.embedding_backward(vals, last, rows, dtable=big)
     _same(big[last], vals, "dtable")
     assert (big[[0, rows // 2, rows - 3]] == 0).all()
+
+
+def test_more_workgroups_than_one_launch_holds():
+    """2^22 + 37 tokens: the row movers' grids are capped there and loop over the rest."""
+    note("2^22 + 37 tokens")
+    T, H = (1 << 22) + 37, 8
+    g = _gen(70)
+    rows = _randn(g, (T, H), BF16)
+    tm = torch.randperm(T, generator=g).to(DEV).view(T, 1)
+    _same(moe.dispatch_backward(rows, tm), rows[tm[:, 0]], "dx")
+    w = torch.full((T, 1), 0.5, device=DEV)
+    dy, dw = moe.combine_backward(rows, rows, tm, w)
+    want = torch.empty_like(rows)
+    want[tm[:, 0]] = rows * 0.5
+    _same(dy, want, "dy")
+    prod = rows.double() * rows[tm[:, 0]].double()
+    _near(dw, prod.sum(1, keepdim=True), prod.abs().sum(1, keepdim=True) * (H / 8 + 17) * U, "dw")
+    _same(moe.embedding(tm[:, 0], rows, scale=2.0), rows[tm[:, 0]] * 2.0, "embedding")
+    _same(moe.embedding_backward(rows, tm[:, 0], T, dtable_dtype=BF16)[tm[:, 0]], rows, "dtable")
 
 
 def test_refusals():

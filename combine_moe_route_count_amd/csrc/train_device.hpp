@@ -1,6 +1,6 @@
 // train_device.hpp - device helpers of the training-side kernels: wave64
-// reductions, the total order of f32 values, and lane-units of 8 row elements
-// in every row format.
+// reductions, lane-units of row elements in every row format, and the mapping of
+// work items to workgroups.
 #pragma once
 
 #include "device_common.hpp"

@@ -344,6 +344,8 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateArgs a,
         const int64_t want = b * kTokens + threadIdx.x / G;
         const bool live = want < a.T;
         const int64_t t = live ? want : a.T - 1;
+        float v[V];
+        if (!a.renorm) load_logits<V, F32>(a.logits, t, a.E, gl, vec, v);
         // lane k: entry k's expert, its logit and the gradient of its weight
         int j = -1;
         float l = -__builtin_inff(), dw = 0.0f;
@@ -356,10 +358,8 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateArgs a,
                 l = load_logit<F32>(a.logits, t * a.E + id);
             }
         }
-        float v[V];
         float top = l;
         if (!a.renorm) {
-            load_logits<V, F32>(a.logits, t, a.E, gl, vec, v);
 #pragma unroll
             for (int i = 0; i < V; ++i) top = fmaxf(top, v[i]);
         }

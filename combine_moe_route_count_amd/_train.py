@@ -272,8 +272,8 @@ def embedding_workspace_size(N: int, V: int, H: int) -> int:
 
 
 def embedding_workspace(N: int, V: int, H: int, device="cuda") -> torch.Tensor:
-    """A device workspace of embedding_backward for these sizes (256-byte aligned,
-    needs no initialisation)."""
+    """A device workspace of embedding_backward for these sizes, and for any smaller N
+    and V of the same H (256-byte aligned, needs no initialisation)."""
     n = max(embedding_workspace_size(N, V, H), 1)
     buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
     off = (-buf.data_ptr()) % 256

@@ -40,12 +40,26 @@ constexpr int kSmallSort = 4096;   // positions
 // gradient: 10136 tokens of 80 35.0 and 39.7 us, 65536 of 64 48.9 and 63.2, 131072 of 256
 // 65.5 and 82.7, 262144 of 256 115 and 131.
 constexpr int64_t kOwnScanTiles = 256;
+constexpr int kDigitMost = 9, kDigitLeast = 4;
+constexpr int64_t kRoutedCounts = (int64_t)1 << 14;
 inline int digit_bits(int64_t tiles) {
-    int bits = 9;
-    while (bits > 4 && (tiles <= kOwnScanTiles ? (tiles * tiles) << bits > (1 << 24)
-                                               : tiles << bits > (1 << 14)))
+    int bits = kDigitMost;
+    while (bits > kDigitLeast && (tiles <= kOwnScanTiles ? (tiles * tiles) << bits > (1 << 24)
+                                                         : tiles << bits > kRoutedCounts))
         --bits;
     return bits;
+}
+
+// Tiles x keys counts that the workspace holds for ids of id_bits: enough for every sort
+// of at most this many tiles, since fewer tiles take longer digits.  Past kLongDigitTiles
+// all digits have kDigitLeast bits.
+constexpr int64_t kLongDigitTiles = kRoutedCounts >> (kDigitLeast + 1);
+inline int64_t count_room(int64_t tiles, int id_bits) {
+    const int most = id_bits < kDigitMost ? id_bits : kDigitMost;
+    const int least = id_bits < kDigitLeast ? id_bits : kDigitLeast;
+    const int64_t few = (tiles < kLongDigitTiles ? tiles : kLongDigitTiles) << most;
+    const int64_t many = tiles << least;
+    return few > many ? few : many;
 }
 
 __device__ __forceinline__ int64_t token_id(const void* ids, int id_bytes, int64_t n) {
@@ -555,11 +569,26 @@ __global__ __launch_bounds__(kEmbThreads) void join_kernel(SumArgs a, int nch, i
 // of 64 - / 44.4 / 39.5 / 39.0, of 264 - / 75.0 / 72.8 / 77.3; 8192 tokens of 1024 over
 // 100 rows 24.0 / 26.2 / 33.8 / -, of 4096 over 200 rows 32.6 / 32.5 / 30.3 / -; 4096
 // of 1024 over 100 rows 23.0 / 27.0 / 26.9 / -.
+constexpr int kShortestWindow = 8;
+inline int64_t enough_windows(int64_t H) {
+    const int64_t waves = H <= 512 ? 2048 : 512, per_row = (H + 511) / 512;
+    return (waves + per_row - 1) / per_row;
+}
 inline int window_of(int64_t N, int64_t H) {
-    const int64_t waves = H <= 512 ? 2048 : 512;
     int w = kWave;
-    while (w > 8 && (N + w - 1) / w * ((H + 511) / 512) < waves) w /= 2;
+    while (w > kShortestWindow && (N + w - 1) / w < enough_windows(H)) w /= 2;
     return w;
+}
+
+// Windows that the workspace holds: enough for every sort of at most N positions, since
+// fewer positions take shorter windows.  A window that was halved leaves less than twice
+// enough_windows, because the longer one left less than enough.
+inline int64_t window_room(int64_t N, int64_t H) {
+    const int64_t full = (N + kWave - 1) / kWave;
+    const int64_t shortest = (N + kShortestWindow - 1) / kShortestWindow;
+    const int64_t halved = 2 * (enough_windows(H) - 1);
+    const int64_t most = shortest < halved ? shortest : halved;
+    return most > full ? most : full;
 }
 
 struct GradWs {
@@ -578,17 +607,19 @@ struct GradWs {
 // 65536 of 64 into 131072 f32 rows 64.0, 67.6; 8192 of 4096 into 50000 rows 164, 159.
 constexpr int64_t kZeroTwice = (int64_t)64 << 20;
 
+// Every piece is sized so that it does not shrink when N or V grows: a workspace for the
+// most positions and the largest vocabulary serves every call of the same H below them.
 GradWs grad_ws(int64_t N, int64_t V, int64_t H) {
     GradWs w{};
+    int id_bits = 1;
     w.tiles = (N + kTile - 1) / kTile;
     w.window = window_of(N, H);
     w.windows = (N + w.window - 1) / w.window;
     if (N > kSmallSort) {
-        int bits = 1;
-        while (((int64_t)1 << bits) < V) ++bits;
+        while (((int64_t)1 << id_bits) < V) ++id_bits;
         const int most = digit_bits(w.tiles);
-        w.passes = (bits + most - 1) / most;
-        w.bits = (bits + w.passes - 1) / w.passes;
+        w.passes = (id_bits + most - 1) / most;
+        w.bits = (id_bits + w.passes - 1) / w.passes;
         w.zero_early = (N < V ? N : V) * H * 4 <= kZeroTwice;
     }
     size_t total = 0;
@@ -597,21 +628,21 @@ GradWs grad_ws(int64_t N, int64_t V, int64_t H) {
         total += (bytes + 255) & ~(size_t)255;
         return at;
     };
-    const size_t n = (size_t)N, nk = (size_t)1 << w.bits;
+    const size_t n = (size_t)N, offsets = 4 * (((size_t)1 << kDigitMost) + 1);
     // the routing's arrival ticket first: calls of any size that share a workspace
     // find it where the last one left it
     w.ticket = take(sizeof(uint64_t));
-    w.off0 = take(4 * (nk + 1));   // its last word: how many ids are valid
+    w.off0 = take(offsets);   // behind the last offset: how many ids are valid
     w.id[0] = take(4 * n);
     w.pos[0] = take(4 * n);
-    w.partial = take(4 * 2 * (size_t)w.windows * (size_t)H);
+    w.partial = take(4 * 2 * (size_t)window_room(N, H) * (size_t)H);
     if (w.passes > 0) {
         w.local_rank = take(4 * n);
-        w.tile_cnt = take(4 * (size_t)w.tiles * nk);
+        w.tile_cnt = take(4 * (size_t)count_room(w.tiles, id_bits));
         w.tile_flags = take(8 * (size_t)w.tiles);
     }
     if (w.passes > 1) {
-        w.off = take(4 * (nk + 1));
+        w.off = take(offsets);
         w.id[1] = take(4 * n);
         w.pos[1] = take(4 * n);
         w.present = take((size_t)V);

@@ -107,8 +107,10 @@ int moe_embedding(const void* table, moe_dtype table_dt, int64_t V, int64_t H, c
                   int32_t* stats, void* stream);
 
 /* Bytes of device workspace that moe_embedding_backward needs for these sizes (0
- * for sizes outside the limits).  It needs no initialisation, may be reused by
- * consecutive calls on one stream, also from a captured graph.  Calls that may run
+ * for sizes outside the limits).  For one H it does not shrink when N or V grows, so a
+ * workspace for the longest batch and the largest table serves every smaller call.  It
+ * needs no initialisation, may be reused by consecutive calls on one stream, of any
+ * sizes it is large enough for, also from a captured graph.  Calls that may run
  * at the same time, or that several host threads enqueue at the same time, need
  * workspaces of their own. */
 size_t moe_embedding_workspace_size(int64_t N, int64_t V, int64_t H);

@@ -353,9 +353,13 @@ __global__ __launch_bounds__(kGateThreads) void gate_backward_kernel(GateArgs a,
             const int32_t id = a.idx[t * a.K + gl];
             const float g = a.dw[t * a.K + gl];
             if (id >= 0 && id < a.E) {
-                j = id;
-                dw = g;
                 l = load_logit<F32>(a.logits, t * a.E + id);
+                // a masked expert's weight is 0 whatever its logit does next: its entry
+                // counts as none, so a non-finite dw there reaches nobody as 0 * dw
+                if (l != -__builtin_inff()) {
+                    j = id;
+                    dw = g;
+                }
             }
         }
         float top = l;

@@ -46,9 +46,9 @@ int moe_gate(const void* logits, moe_dtype l_dt, int64_t T, int E, int K, int re
  *   renormalize != 0:  dlogits[t,j] = sum over k with idx_k = j of (d_k - p_k*D);
  *                      0 for every expert that was not chosen
  *   renormalize == 0:  dlogits[t,j] = sum over k with idx_k = j of d_k, - p_j*D
- * idx values outside [0,E) are skipped whatever their dw holds; a token whose
- * softmax runs over nothing but -inf gets zeros; an expert named twice gets both
- * entries' gradients.
+ * Entries whose idx is outside [0,E), or whose expert's logit is -inf, are skipped
+ * whatever their dw holds; a token whose softmax runs over nothing but -inf gets
+ * zeros; an expert named twice gets both entries' gradients.
  *   logits  [T,E] l_dt, as given to moe_gate
  *   idx     int32 [T,K]; dw f32 [T,K]
  *   dlogits out [T,E] l_dt */

@@ -48,7 +48,8 @@ int moe_gate(const void* logits, moe_dtype l_dt, int64_t T, int E, int K, int re
  *   renormalize == 0:  dlogits[t,j] = sum over k with idx_k = j of d_k, - p_j*D
  * Entries whose idx is outside [0,E), or whose expert's logit is -inf, are skipped
  * whatever their dw holds; a token whose softmax runs over nothing but -inf gets
- * zeros; an expert named twice gets both entries' gradients.
+ * zeros.  "The chosen" are the entries: an expert named twice, which moe_gate never
+ * does, stands twice in the softmax of renormalize and gets both entries' gradients.
  *   logits  [T,E] l_dt, as given to moe_gate
  *   idx     int32 [T,K]; dw f32 [T,K]
  *   dlogits out [T,E] l_dt */

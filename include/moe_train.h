@@ -69,8 +69,9 @@ int moe_gate_backward(const void* logits, moe_dtype l_dt, int64_t T, int E, int 
  *   y             [y_rows,H] y_dt (any of the four; fp4: [y_rows,H/2] bytes); may be
  *                 NULL when dw is NULL
  *   y_scales      f32 [y_rows,H/128] or NULL; only with MOE_FP8_E4M3 / MOE_FP4_E2M1
- *   tok_map       int64 [T,K]; each row at most once, as every dispatch writes it
- *                 (a row named twice gets one of its writers)
+ *   tok_map       int64 [T,K]; each row at most once, as every dispatch writes it.
+ *                 (The entries of a row named twice have their dw; each element of
+ *                 its dy comes from one of them, which one is not fixed.)
  *   w             f32 [T,K]; may be NULL when dy is NULL
  *   dy            out [y_rows,H] dy_dt (MOE_BF16 or MOE_F32), or NULL: not computed
  *   packed_cnt, packed_off  int32 [E], [E+1] as the dispatch wrote them, or both NULL.

@@ -58,7 +58,9 @@ __device__ __forceinline__ void zero_gap(const CombineGradArgs& a, int64_t item,
 // in flight decides: two bf16 or f32 rows at up to 512 threads, four rows of codes
 // at up to 256.  Measured (us) at T=8192 K=8 H=7168 bf16: 1 entry 464, 2 367-369, 4
 // 377, a wave per entry 382; T=8192 K=6 H=4096 f32: 2 entries 352-360, 4 407, a wave
-// per entry 391; e4m3 rows T=8192 K=8 H=7168: 2 entries 326, 4 311-313.
+// per entry 391.  Codes, e4m3 and e2m1: T=8192 K=8 H=7168 2 entries 319 and 293, 4 entries
+// 313 and 264, at up to 512 threads 366 and 383, 310 and 264; T=501 K=8 H=6144 2 entries
+// 21.3 and 21.3, 4 entries 18.4 and 17.6, at up to 512 threads 25.4 and 25.7, 20.0 and 19.8.
 constexpr bool is_quant(RowKind k) { return k == RowKind::Fp8 || k == RowKind::Fp4; }
 constexpr int grad_entries(RowKind k) { return is_quant(k) ? 4 : 2; }
 constexpr int grad_threads(RowKind k) { return is_quant(k) ? 256 : kGradThreads; }

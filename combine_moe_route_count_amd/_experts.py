@@ -1,0 +1,158 @@
+"""ctypes binding of the experts' step of libmoe_route.so (include/moe_experts.h):
+MXFP4 quantization, SwiGLU with its 8-bit checkpoint, and its gradient.  Argument
+marshalling only; the library's checks raise MoeError, and what only the tensors can
+show (type, shape, contiguity, device) raises ValueError before the call.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from ._lib import MOE_FP8_E4M3, load, ptr
+from ._train import _FLOAT, _QUANT, _call_fn, _dim, _gpu, _need, _tensor
+
+_P = ctypes.c_void_p
+_I64 = ctypes.c_int64
+_I32 = ctypes.c_int
+
+_SIGNATURES = {
+    "moe_mxfp4_quantize": [_P, _I32, _I64, _I64, _P, _P, _P],
+    "moe_mxfp4_dequantize": [_P, _P, _I64, _I64, _P, _I32, _P],
+    "moe_swiglu": [_P, _I32, _I64, _I64, _P, _P, _I32, _P, _I32, _P, _P, _P],
+    "moe_swiglu_backward": [_P, _I32, _P, _I32, _P, _I64, _I64, _P, _P, _I32, _P, _P, _I32, _P],
+}
+
+_BYTE = (torch.uint8,)
+_bound = None
+
+
+def _lib() -> ctypes.CDLL:
+    """The library with the signatures of the experts' step set (once)."""
+    global _bound
+    if _bound is None:
+        lib = load()
+        for name, args in _SIGNATURES.items():
+            fn = getattr(lib, name)
+            fn.argtypes = args
+            fn.restype = ctypes.c_int
+        _bound = lib
+    return _bound
+
+
+def _call(name: str, dev: int, *args) -> None:
+    _call_fn(getattr(_bound or _lib(), name), dev, *args)
+
+
+def _segments(packed_cnt, packed_off, dev: int) -> int:
+    """E of the segments, 0 if there are none."""
+    _need((packed_cnt is None) == (packed_off is None), "packed_cnt and packed_off go together")
+    if packed_cnt is None:
+        return 0
+    E = _dim("packed_cnt", packed_cnt, 1, 0)
+    _tensor("packed_cnt", packed_cnt, (E,), (torch.int32,), dev)
+    _tensor("packed_off", packed_off, (E + 1,), (torch.int32,), dev)
+    return E
+
+
+def mxfp4_quantize(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                   scales: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """x [rows,H] (bf16 or f32, H % 32 == 0) as MXFP4: uint8 codes [rows,H/2], two e2m1
+    codes per byte, and uint8 scales [rows,H/32], the e8m0 exponents of the blocks of 32.
+    Expert weights [E,N,H] go as w.view(E * N, H)."""
+    dev = _gpu("x", x, 2)
+    rows, H = x.shape
+    _tensor("x", x, (rows, H), _FLOAT, dev)
+    if codes is None:
+        codes = torch.empty((rows, H // 2), dtype=torch.uint8, device=dev)
+    else:
+        _tensor("codes", codes, (rows, H // 2), _BYTE, dev)
+    if scales is None:
+        scales = torch.empty((rows, H // 32), dtype=torch.uint8, device=dev)
+    else:
+        _tensor("scales", scales, (rows, H // 32), _BYTE, dev)
+    _call("moe_mxfp4_quantize", dev, ptr(x), _FLOAT[x.dtype], rows, H, ptr(codes), ptr(scales))
+    return codes, scales
+
+
+def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor,
+                     out_dtype: torch.dtype = torch.bfloat16,
+                     y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values [rows,H] (bf16 or f32) of MXFP4 codes [rows,H/2] and scales [rows,H/32]."""
+    dev = _gpu("codes", codes, 2)
+    rows, H = codes.shape[0], 2 * codes.shape[1]
+    _tensor("codes", codes, (rows, H // 2), _BYTE, dev)
+    _tensor("scales", scales, (rows, H // 32), _BYTE, dev)
+    if y is None:
+        y = torch.empty((rows, H), dtype=out_dtype, device=dev)
+    _tensor("y", y, (rows, H), _FLOAT, dev)
+    _call("moe_mxfp4_dequantize", dev, ptr(codes), ptr(scales), rows, H, ptr(y), _FLOAT[y.dtype])
+    return y
+
+
+def swiglu(gu: torch.Tensor, packed_cnt: Optional[torch.Tensor] = None,
+           packed_off: Optional[torch.Tensor] = None, save: bool = False,
+           h: Optional[torch.Tensor] = None, h_dtype: Optional[torch.dtype] = None,
+           codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+    """h [rows,I] = silu(gu[:, :I]) * gu[:, I:], of gu's type unless h or h_dtype says
+    otherwise.  save=True returns (h, codes, scales) with the 8-bit checkpoint of gu that
+    swiglu_backward takes: uint8 e4m3 codes [rows,2I] and f32 scales [rows,2I/128]
+    (I % 128 == 0; fp8_dequant gives its values).  With the dispatch's packed_cnt and
+    packed_off only rows that an expert owns are read and written."""
+    dev = _gpu("gu", gu, 2)
+    rows, I = gu.shape[0], gu.shape[1] // 2
+    _tensor("gu", gu, (rows, 2 * I), _FLOAT, dev)
+    E = _segments(packed_cnt, packed_off, dev)
+    if h is None:
+        h = torch.empty((rows, I), dtype=h_dtype or gu.dtype, device=dev)
+    _tensor("h", h, (rows, I), _FLOAT, dev)
+    _need(save or (codes is None and scales is None), "codes and scales need save=True")
+    if save:
+        if codes is None:
+            codes = torch.empty((rows, 2 * I), dtype=torch.uint8, device=dev)
+        else:
+            _tensor("codes", codes, (rows, 2 * I), _BYTE, dev)
+        if scales is None:
+            scales = torch.empty((rows, 2 * I // 128), dtype=torch.float32, device=dev)
+        else:
+            _tensor("scales", scales, (rows, 2 * I // 128), (torch.float32,), dev)
+    if rows:    # an empty tensor has no address
+        _call("moe_swiglu", dev, ptr(gu), _FLOAT[gu.dtype], rows, I, ptr(packed_cnt),
+              ptr(packed_off), E, ptr(h), _FLOAT[h.dtype], ptr(codes), ptr(scales))
+    return (h, codes, scales) if save else h
+
+
+def swiglu_backward(dh: torch.Tensor, gu: torch.Tensor, scales: Optional[torch.Tensor] = None,
+                    packed_cnt: Optional[torch.Tensor] = None,
+                    packed_off: Optional[torch.Tensor] = None,
+                    dgu: Optional[torch.Tensor] = None, dgu_dtype: Optional[torch.dtype] = None,
+                    h: Optional[torch.Tensor] = None, want_h: bool = True
+                    ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Gradient of swiglu: (dgu [rows,2I], h [rows,I]) from dh [rows,I] and gu, which is
+    what swiglu read (bf16 or f32) or its checkpoint (uint8 codes, with scales).  dgu has
+    dh's type unless dgu or dgu_dtype says otherwise; h, of dgu's type, is the activation
+    again, for the gradient of the second product (want_h=False leaves it out)."""
+    dev = _gpu("dh", dh, 2)
+    rows, I = dh.shape
+    _tensor("dh", dh, (rows, I), _FLOAT, dev)
+    quant = gu.dtype in _QUANT
+    _tensor("gu", gu, (rows, 2 * I), _QUANT if quant else _FLOAT, dev)
+    _need(quant == (scales is not None), "scales go with uint8 codes, and with nothing else")
+    if quant:
+        _tensor("scales", scales, (rows, 2 * I // 128), (torch.float32,), dev)
+    E = _segments(packed_cnt, packed_off, dev)
+    if dgu is None:
+        dgu = torch.empty((rows, 2 * I), dtype=dgu_dtype or dh.dtype, device=dev)
+    _tensor("dgu", dgu, (rows, 2 * I), _FLOAT, dev)
+    if not want_h:
+        h = None
+    elif h is None:
+        h = torch.empty((rows, I), dtype=dgu.dtype, device=dev)
+    if h is not None:
+        _tensor("h", h, (rows, I), (dgu.dtype,), dev)
+    if rows:
+        _call("moe_swiglu_backward", dev, ptr(dh), _FLOAT[dh.dtype], ptr(gu),
+              MOE_FP8_E4M3 if quant else _FLOAT[gu.dtype], ptr(scales), rows, I, ptr(packed_cnt),
+              ptr(packed_off), E, ptr(dgu), ptr(h), _FLOAT[dgu.dtype])
+    return dgu, h

@@ -98,9 +98,8 @@ def _stream_of(dev: int):
     return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
-def _call(name: str, dev: int, *args) -> None:
-    """The library call on GPU dev's current stream, with dev current."""
-    fn = getattr(_bound or _lib(), name)
+def _call_fn(fn, dev: int, *args) -> None:
+    """The library call fn on GPU dev's current stream, with dev current."""
     if dev == _current_device():
         status = fn(*args, _stream_of(dev))
     else:
@@ -108,6 +107,10 @@ def _call(name: str, dev: int, *args) -> None:
             status = fn(*args, _stream_of(dev))
     if status:
         _check(status)
+
+
+def _call(name: str, dev: int, *args) -> None:
+    _call_fn(getattr(_bound or _lib(), name), dev, *args)
 
 
 def gate(logits: torch.Tensor, K: int, renormalize: bool = True, scale: float = 1.0,

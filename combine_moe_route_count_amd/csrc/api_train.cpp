@@ -12,36 +12,16 @@
 namespace {
 
 using moe::aligned;
+using moe::check_apart;
+using moe::check_elems;
+using moe::check_float;
 using moe::check_H;
+using moe::check_row_count;
 using moe::check_rows_ptr;
 using moe::fail;
+using moe::float_bytes;
+using moe::is_float;
 using moe::kMaxRows;
-
-bool is_float(moe_dtype d) { return d == MOE_BF16 || d == MOE_F32; }
-
-int64_t float_bytes(moe_dtype d) { return d == MOE_F32 ? 4 : 2; }
-
-int check_float(moe_dtype d, const char* name) {
-    if (is_float(d)) return MOE_OK;
-    return fail(MOE_ERR_INVALID_ARG, "%s dtype must be MOE_BF16 or MOE_F32", name);
-}
-
-int check_elems(const void* p, int64_t n, size_t align, const char* name) {
-    if (n > 0 && !p) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
-    if (p && !aligned(p, align))
-        return fail(MOE_ERR_INVALID_ARG, "%s is not %zu-byte aligned", name, align);
-    return MOE_OK;
-}
-
-// out and in must not share bytes.
-int check_apart(const void* out, int64_t out_bytes, const char* out_name, const void* in,
-                int64_t in_bytes, const char* in_name) {
-    if (!out || !in || out_bytes <= 0 || in_bytes <= 0) return MOE_OK;
-    const uintptr_t a = (uintptr_t)out, b = (uintptr_t)in;
-    if (a < b + (uintptr_t)in_bytes && b < a + (uintptr_t)out_bytes)
-        return fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", out_name, in_name);
-    return MOE_OK;
-}
 
 int check_entries(int64_t T, int K, const int64_t* tok_map) {
     if (T < 0 || T >= ((int64_t)1 << 31))
@@ -50,12 +30,6 @@ int check_entries(int64_t T, int K, const int64_t* tok_map) {
     if (T * (int64_t)K >= ((int64_t)1 << 31))
         return fail(MOE_ERR_INVALID_ARG, "T*K=%lld must be < 2^31", (long long)(T * K));
     return check_elems(tok_map, T, 8, "tok_map");
-}
-
-int check_row_count(int64_t rows, const char* name) {
-    if (rows < 0 || rows > kMaxRows)
-        return fail(MOE_ERR_INVALID_ARG, "%s must be in [0, 2^31-1]", name);
-    return MOE_OK;
 }
 
 int check_gate(const void* logits, moe_dtype l_dt, int64_t T, int E, int K) {

@@ -1,5 +1,5 @@
 """ctypes binding of the experts' step of libmoe_route.so (include/moe_experts.h):
-MXFP4 quantization, SwiGLU with its 8-bit checkpoint, and its gradient.  Argument
+MXFP4 quantization and the grouped product on it, SwiGLU with its 8-bit checkpoint, and its gradient.  Argument
 marshalling only; the library's checks raise MoeError, and what only the tensors can
 show (type, shape, contiguity, device) raises ValueError before the call.
 """
@@ -20,6 +20,7 @@ _I32 = ctypes.c_int
 _SIGNATURES = {
     "moe_mxfp4_quantize": [_P, _I32, _I64, _I64, _P, _P, _P],
     "moe_mxfp4_dequantize": [_P, _P, _I64, _I64, _P, _I32, _P],
+    "moe_expert_product_mxfp4": [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _I32, _I32, _P, _I32, _P],
     "moe_swiglu": [_P, _I32, _I64, _I64, _P, _P, _I32, _P, _I32, _P, _P, _P],
     "moe_swiglu_backward": [_P, _I32, _P, _I32, _P, _I64, _I64, _P, _P, _I32, _P, _P, _I32, _P],
 }
@@ -88,6 +89,34 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor,
         y = torch.empty((rows, H), dtype=out_dtype, device=dev)
     _tensor("y", y, (rows, H), _FLOAT, dev)
     _call("moe_mxfp4_dequantize", dev, ptr(codes), ptr(scales), rows, H, ptr(y), _FLOAT[y.dtype])
+    return y
+
+
+def expert_product_mxfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor,
+                         w_scales: torch.Tensor, packed_cnt: torch.Tensor,
+                         packed_off: torch.Tensor, swiglu: bool = False,
+                         y: Optional[torch.Tensor] = None,
+                         out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """y [rows,N]: every packed row times its expert's weights, both MXFP4: a uint8
+    [rows,H/2] with a_scales [rows,H/32], w uint8 [E,N,H/2] with w_scales [E,N,H/32].
+    swiglu=True: w holds N/2 gate rows and then N/2 up rows of each expert, and y
+    [rows,N/2] is silu(gate) * up.  Rows that no expert owns (packed_cnt, packed_off as
+    the dispatch wrote them) are not written: give y where they must hold something."""
+    dev = _gpu("a", a, 2)
+    rows, H = a.shape[0], 2 * a.shape[1]
+    E, N = _dim("w", w, 3, 0), w.shape[1]
+    _tensor("a", a, (rows, H // 2), _BYTE, dev)
+    _tensor("a_scales", a_scales, (rows, H // 32), _BYTE, dev)
+    _tensor("w", w, (E, N, H // 2), _BYTE, dev)
+    _tensor("w_scales", w_scales, (E, N, H // 32), _BYTE, dev)
+    _tensor("packed_cnt", packed_cnt, (E,), (torch.int32,), dev)
+    _tensor("packed_off", packed_off, (E + 1,), (torch.int32,), dev)
+    cols = N // 2 if swiglu else N
+    if y is None:
+        y = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+    _tensor("y", y, (rows, cols), _FLOAT, dev)
+    _call("moe_expert_product_mxfp4", dev, ptr(a), ptr(a_scales), rows, H, ptr(w), ptr(w_scales), N,
+          ptr(packed_cnt), ptr(packed_off), E, int(swiglu), ptr(y), _FLOAT[y.dtype])
     return y
 
 

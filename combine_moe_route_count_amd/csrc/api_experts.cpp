@@ -95,6 +95,46 @@ MOE_API int moe_mxfp4_dequantize(const void* codes, const void* scales, int64_t 
     return MOE_OK;
 }
 
+MOE_API int moe_expert_product_mxfp4(const void* a, const void* a_scales, int64_t rows, int64_t H,
+                                     const void* w, const void* w_scales, int64_t N,
+                                     const int32_t* packed_cnt, const int32_t* packed_off, int E,
+                                     int swiglu, void* y, moe_dtype y_dt, void* stream) {
+    MOE_TRY(check_float(y_dt, "y"));
+    MOE_TRY(check_len(H, moe::kMxBlock, "H"));
+    MOE_TRY(check_len(N, swiglu ? 16 : 8, "N"));
+    MOE_TRY(check_row_count(rows, "rows"));
+    MOE_TRY(check_segments(packed_cnt, packed_off, E, true));
+    MOE_TRY(check_rows_ptr(a, rows, "a"));
+    MOE_TRY(check_elems(a_scales, rows, 1, "a_scales"));
+    MOE_TRY(check_rows_ptr(w, E, "w"));
+    MOE_TRY(check_elems(w_scales, E, 1, "w_scales"));
+    MOE_TRY(check_rows_ptr(y, rows, "y"));
+    const int64_t cols = swiglu ? N / 2 : N;
+    MOE_TRY(check_all_apart({{y, rows * cols * float_bytes(y_dt), "y"}},
+                            {{a, rows * (H / 2), "a"},
+                             {a_scales, rows * (H / moe::kMxBlock), "a_scales"},
+                             {w, E * N * (H / 2), "w"},
+                             {w_scales, E * N * (H / moe::kMxBlock), "w_scales"},
+                             {packed_cnt, (int64_t)E * 4, "packed_cnt"},
+                             {packed_off, ((int64_t)E + 1) * 4, "packed_off"}}));
+    moe::ProductArgs p{};
+    p.a = (const uint8_t*)a;
+    p.a_scales = (const uint8_t*)a_scales;
+    p.w = (const uint8_t*)w;
+    p.w_scales = (const uint8_t*)w_scales;
+    p.rows = rows;
+    p.H = H;
+    p.N = N;
+    p.packed_cnt = packed_cnt;
+    p.packed_off = packed_off;
+    p.E = E;
+    p.swiglu = swiglu != 0;
+    p.y = y;
+    p.y_f32 = y_dt == MOE_F32;
+    MOE_HIP(moe::launch_product(p, (hipStream_t)stream), "moe_expert_product_mxfp4");
+    return MOE_OK;
+}
+
 MOE_API int moe_swiglu(const void* gu, moe_dtype gu_dt, int64_t rows, int64_t I,
                        const int32_t* packed_cnt, const int32_t* packed_off, int E, void* h,
                        moe_dtype h_dt, void* codes, float* scales, void* stream) {

@@ -49,4 +49,19 @@ struct SwigluGradArgs {
 };
 hipError_t launch_swiglu_grad(const SwigluGradArgs& a, hipStream_t s);
 
+struct ProductArgs {
+    const uint8_t* a;           // [rows,H/2] codes, a_scales [rows,H/32]
+    const uint8_t* a_scales;
+    const uint8_t* w;           // [E,N,H/2] codes, w_scales [E,N,H/32]
+    const uint8_t* w_scales;
+    int64_t rows, H, N;
+    const int32_t* packed_cnt;  // [E]
+    const int32_t* packed_off;  // [E+1]
+    int E;
+    bool swiglu;
+    void* y;                    // [rows,N], or [rows,N/2] with swiglu
+    bool y_f32;
+};
+hipError_t launch_product(const ProductArgs& a, hipStream_t s);
+
 }  // namespace moe

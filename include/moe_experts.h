@@ -51,6 +51,22 @@ int moe_mxfp4_quantize(const void* x, moe_dtype x_dt, int64_t rows, int64_t H, v
 int moe_mxfp4_dequantize(const void* codes, const void* scales, int64_t rows, int64_t H, void* y,
                          moe_dtype y_dt, void* stream);
 
+/* The product of packed rows with their experts' weights, both in MXFP4 (sums in f32):
+ *   y[r,n] = sum_h a[r,h] * w[e,n,h]     for every row r of expert e's segment
+ * or, with swiglu != 0, where a weight matrix is I gate rows and then I up rows, N = 2I:
+ *   y[r,i] = silu(sum_h a[r,h] * w[e,i,h]) * sum_h a[r,h] * w[e,I+i,h]
+ * E = 1 with one segment is an ordinary product.  Segments that overlap, which no
+ * dispatch makes, leave the rows they share with the result of one of their experts.
+ *   a, a_scales  [rows,H/2] codes (16-byte aligned), [rows,H/32] scales, H % 32 == 0
+ *   w, w_scales  [E,N,H/2] codes (16-byte aligned), [E,N,H/32] scales,
+ *           N % 8 == 0 (N % 16 == 0 with swiglu), N <= 2^24
+ *   packed_cnt, packed_off  the segments
+ *   y       out [rows,N] (swiglu: [rows,N/2]) y_dt (MOE_BF16 or MOE_F32) */
+int moe_expert_product_mxfp4(const void* a, const void* a_scales, int64_t rows, int64_t H,
+                             const void* w, const void* w_scales, int64_t N,
+                             const int32_t* packed_cnt, const int32_t* packed_off, int E,
+                             int swiglu, void* y, moe_dtype y_dt, void* stream);
+
 /* SwiGLU of packed rows, h[r,i] = silu(gu[r,i]) * gu[r,I+i], silu(g) = g / (1 + exp(-g)),
  * and on request the 8-bit checkpoint of gu that moe_swiglu_backward takes.
  *   gu      [rows,2I] gu_dt (MOE_BF16 or MOE_F32), I % 8 == 0

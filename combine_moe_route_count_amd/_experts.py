@@ -1,7 +1,8 @@
 """ctypes binding of the experts' step of libmoe_route.so (include/moe_experts.h):
-MXFP4 quantization and the grouped product on it, SwiGLU with its 8-bit checkpoint, and its gradient.  Argument
-marshalling only; the library's checks raise MoeError, and what only the tensors can
-show (type, shape, contiguity, device) raises ValueError before the call.
+MXFP4 quantization and the grouped product on it, the whole step for a few tokens,
+SwiGLU with its 8-bit checkpoint, and its gradient.  Argument marshalling only; the
+library's checks raise MoeError, and what only the tensors can show (type, shape,
+contiguity, device) raises ValueError before the call.
 """
 from __future__ import annotations
 
@@ -10,17 +11,20 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._lib import MOE_FP8_E4M3, load, ptr
+from ._lib import MOE_BF16, MOE_FP4_E2M1, MOE_FP8_E4M3, load, ptr
 from ._train import _FLOAT, _QUANT, _call_fn, _dim, _gpu, _need, _tensor
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int
+_SZ = ctypes.c_size_t
 
 _SIGNATURES = {
     "moe_mxfp4_quantize": [_P, _I32, _I64, _I64, _P, _P, _P],
     "moe_mxfp4_dequantize": [_P, _P, _I64, _I64, _P, _I32, _P],
     "moe_expert_product_mxfp4": [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _I32, _I32, _P, _I32, _P],
+    "moe_experts_decode": [_P, _I64, _I64, _P, _P, _I32, _I32, _I64, _P, _P, _P, _P, _I32, _P, _I32,
+                           _P, _SZ, _P],
     "moe_swiglu": [_P, _I32, _I64, _I64, _P, _P, _I32, _P, _I32, _P, _P, _P],
     "moe_swiglu_backward": [_P, _I32, _P, _I32, _P, _I64, _I64, _P, _P, _I32, _P, _P, _I32, _P],
 }
@@ -38,6 +42,8 @@ def _lib() -> ctypes.CDLL:
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = ctypes.c_int
+        lib.moe_experts_decode_workspace_size.argtypes = [_I64, _I32, _I64]
+        lib.moe_experts_decode_workspace_size.restype = _SZ
         _bound = lib
     return _bound
 
@@ -118,6 +124,58 @@ def expert_product_mxfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
     _call("moe_expert_product_mxfp4", dev, ptr(a), ptr(a_scales), rows, H, ptr(w), ptr(w_scales), N,
           ptr(packed_cnt), ptr(packed_off), E, int(swiglu), ptr(y), _FLOAT[y.dtype])
     return y
+
+
+def experts_decode_workspace_size(T: int, K: int, I: int) -> int:
+    return int(_lib().moe_experts_decode_workspace_size(T, K, I))
+
+
+def experts_decode_workspace(T: int, K: int, I: int, device="cuda") -> torch.Tensor:
+    """A device workspace of experts_decode for these sizes, and for any smaller ones
+    (256-byte aligned, needs no initialisation)."""
+    n = max(experts_decode_workspace_size(T, K, I), 1)
+    buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    off = (-buf.data_ptr()) % 256
+    return buf[off:off + n]
+
+
+def experts_decode(x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, w13: torch.Tensor,
+                   w2: torch.Tensor, w13_scales: Optional[torch.Tensor] = None,
+                   w2_scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   out_dtype: torch.dtype = torch.bfloat16,
+                   ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The whole experts' step of a few tokens (T*K <= 1024): out [T,H] = sum over k of
+    w[t,k] * W2[e] (silu(W1[e] x[t]) * (W3[e] x[t])) with e = idx[t,k].  x bf16 [T,H], idx
+    int32 and w f32 [T,K] as the gate makes them; w13 [E,2I,H] (W1's rows, then W3's) and w2
+    [E,H,I] in bf16, or as MXFP4 codes [E,2I,H/2] and [E,H,I/2] with their scales."""
+    dev = _gpu("x", x, 2)
+    T, H = x.shape
+    K = _dim("idx", idx, 2, 1)
+    E, I = _dim("w13", w13, 3, 0), w13.shape[1] // 2
+    _tensor("x", x, (T, H), (torch.bfloat16,), dev)
+    _tensor("idx", idx, (T, K), (torch.int32,), dev)
+    _tensor("w", w, (T, K), (torch.float32,), dev)
+    mx = w13_scales is not None
+    _need(mx == (w2_scales is not None), "w13_scales and w2_scales go together")
+    pack = 2 if mx else 1
+    types = _BYTE if mx else (torch.bfloat16,)
+    _tensor("w13", w13, (E, 2 * I, H // pack), types, dev)
+    _tensor("w2", w2, (E, H, I // pack), types, dev)
+    if mx:
+        _tensor("w13_scales", w13_scales, (E, 2 * I, H // 32), _BYTE, dev)
+        _tensor("w2_scales", w2_scales, (E, H, I // 32), _BYTE, dev)
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype, device=dev)
+    _tensor("out", out, (T, H), _FLOAT, dev)
+    if ws is None:
+        ws = experts_decode_workspace(T, K, I, torch.device("cuda", dev))
+    else:
+        _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.is_cuda and ws.get_device() == dev,
+              f"ws must be contiguous uint8 on cuda:{dev}")
+    _call("moe_experts_decode", dev, ptr(x), T, H, ptr(idx), ptr(w), K, E, I, ptr(w13),
+          ptr(w13_scales), ptr(w2), ptr(w2_scales), MOE_FP4_E2M1 if mx else MOE_BF16, ptr(out),
+          _FLOAT[out.dtype], ptr(ws), ws.numel())
+    return out
 
 
 def swiglu(gu: torch.Tensor, packed_cnt: Optional[torch.Tensor] = None,

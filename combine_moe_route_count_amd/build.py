@@ -17,7 +17,8 @@ LIB = os.path.join(HERE, "libmoe_route.so")
 
 SOURCES = ["api.cpp", "geometry.cpp", "route.hip", "scatter.hip", "combine.hip", "route_fused.hip",
            "scratch.hip", "api_train.cpp", "gate.hip", "grad.hip", "embedding.hip",
-           "api_experts.cpp", "mxfp4.hip", "swiglu.hip", "expert_product.hip"]
+           "api_experts.cpp", "mxfp4.hip", "swiglu.hip", "expert_product.hip",
+           "experts_decode.hip"]
 HEADERS = ["api_common.hpp", "device_common.hpp", "experts.hpp", "internal.hpp", "route_device.hpp",
            "rows_device.hpp", "train.hpp", "train_device.hpp"]
 

@@ -135,6 +135,68 @@ MOE_API int moe_expert_product_mxfp4(const void* a, const void* a_scales, int64_
     return MOE_OK;
 }
 
+MOE_API size_t moe_experts_decode_workspace_size(int64_t T, int K, int64_t I) {
+    if (T < 0 || K < 1 || K > 16 || T > moe::kDecodeEntries || T * K > moe::kDecodeEntries || I <= 0 ||
+        I % 8 != 0 || I > ((int64_t)1 << 24))
+        return 0;
+    return moe::decode_ws(T, K, I);
+}
+
+MOE_API int moe_experts_decode(const void* x, int64_t T, int64_t H, const int32_t* idx,
+                               const float* w, int K, int E, int64_t I, const void* w13,
+                               const void* w13_scales, const void* w2, const void* w2_scales,
+                               moe_dtype wt_dt, void* out, moe_dtype out_dt, void* ws,
+                               size_t ws_bytes, void* stream) {
+    MOE_TRY(check_float(out_dt, "out"));
+    const bool mx = wt_dt == MOE_FP4_E2M1;
+    if (!mx && wt_dt != MOE_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "weight dtype must be MOE_BF16 or MOE_FP4_E2M1");
+    MOE_TRY(check_len(H, mx ? moe::kMxBlock : 8, "H"));
+    MOE_TRY(check_len(I, mx ? moe::kMxBlock : 8, "I"));
+    if (K < 1 || K > 16) return fail(MOE_ERR_INVALID_ARG, "K=%d must be in [1,16]", K);
+    if (T < 0 || T > moe::kDecodeEntries || T * K > moe::kDecodeEntries)
+        return fail(MOE_ERR_INVALID_ARG, "T=%lld with K=%d: T*K must be in [0, %d]", (long long)T, K,
+                    moe::kDecodeEntries);
+    if (E < 1 || E > 1024) return fail(MOE_ERR_INVALID_ARG, "E=%d must be in [1,1024]", E);
+    MOE_TRY(check_rows_ptr(x, T, "x"));
+    MOE_TRY(check_elems(idx, T, 4, "idx"));
+    MOE_TRY(check_elems(w, T, 4, "w"));
+    MOE_TRY(check_rows_ptr(w13, E, "w13"));
+    MOE_TRY(check_rows_ptr(w2, E, "w2"));
+    if (mx != (w13_scales != nullptr) || mx != (w2_scales != nullptr))
+        return fail(MOE_ERR_INVALID_ARG, "w13_scales and w2_scales go with MOE_FP4_E2M1 weights alone");
+    MOE_TRY(check_rows_ptr(out, T, "out"));
+    const size_t need = moe::decode_ws(T, K, I);
+    MOE_TRY(moe::check_ws(ws, ws_bytes, need));
+    const int64_t wb = (int64_t)E * H * I * (mx ? 1 : 4) / 2, sb = (int64_t)E * H * I / moe::kMxBlock;
+    MOE_TRY(check_all_apart({{out, T * H * float_bytes(out_dt), "out"}, {ws, (int64_t)need, "ws"}},
+                            {{x, T * H * 2, "x"},
+                             {idx, T * K * 4, "idx"},
+                             {w, T * K * 4, "w"},
+                             {w13, 2 * wb, "w13"},
+                             {w13_scales, 2 * sb, "w13_scales"},
+                             {w2, wb, "w2"},
+                             {w2_scales, sb, "w2_scales"}}));
+    moe::DecodeArgs a{};
+    a.x = (const uint16_t*)x;
+    a.T = T;
+    a.H = H;
+    a.I = I;
+    a.idx = idx;
+    a.w = w;
+    a.K = K;
+    a.E = E;
+    a.w13 = w13;
+    a.s13 = (const uint8_t*)w13_scales;
+    a.w2 = w2;
+    a.s2 = (const uint8_t*)w2_scales;
+    a.out = out;
+    a.out_f32 = out_dt == MOE_F32;
+    a.ws = ws;
+    MOE_HIP(moe::launch_experts_decode(a, (hipStream_t)stream), "moe_experts_decode");
+    return MOE_OK;
+}
+
 MOE_API int moe_swiglu(const void* gu, moe_dtype gu_dt, int64_t rows, int64_t I,
                        const int32_t* packed_cnt, const int32_t* packed_off, int E, void* h,
                        moe_dtype h_dt, void* codes, float* scales, void* stream) {

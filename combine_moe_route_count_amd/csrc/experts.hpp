@@ -64,4 +64,23 @@ struct ProductArgs {
 };
 hipError_t launch_product(const ProductArgs& a, hipStream_t s);
 
+// The whole experts' step of a few tokens.
+constexpr int kDecodeEntries = 1024;   // most T*K
+struct DecodeArgs {
+    const uint16_t* x;          // [T,H] bf16
+    int64_t T, H, I;
+    const int32_t* idx;         // [T,K]
+    const float* w;             // [T,K]
+    int K, E;
+    const void* w13;            // [E,2I,H] bf16, or codes with s13 [E,2I,H/32]
+    const uint8_t* s13;
+    const void* w2;             // [E,H,I] bf16, or codes with s2 [E,H,I/32]
+    const uint8_t* s2;
+    void* out;                  // [T,H]
+    bool out_f32;
+    void* ws;
+};
+size_t decode_ws(int64_t T, int K, int64_t I);
+hipError_t launch_experts_decode(const DecodeArgs& a, hipStream_t s);
+
 }  // namespace moe

@@ -2,24 +2,24 @@
 // both in MXFP4: y[r,n] = sum_h a[r,h] * w[e,n,h] for the rows r of expert e's segment,
 // or, with SwiGLU, silu(y[r,i]) * y[r,I+i].
 //
-// Products of codes run on the scaled matrix instruction, which multiplies 16x128 by
-// 128x16 e2m1 codes, applies the two e8m0 scales of each block of 32 and adds in f32.
+// Products of codes run on the scaled matrix instruction, which multiplies 32x64 by
+// 64x32 e2m1 codes, applies the two e8m0 scales of each block of 32 and adds in f32.
 // Weights are its rows and activations its columns, so a lane ends up with 4
 // consecutive n of one row.
 //
 // A workgroup of 4 waves owns BM rows of one expert and 256 weight rows (with SwiGLU
-// 128 gate and 128 up rows, 16 of each in turn, so a lane holds both halves of its
+// 128 gate and 128 up rows, 32 of each in turn, so a lane holds both halves of its
 // outputs).  Which expert a workgroup has follows from packed_cnt on the device; the
 // grid covers the most tiles that the row count allows, and the rest leave at once.
 //
 // K runs in stages of 256 elements: 128 bytes of each row, loaded straight into LDS
 // while the stage before is multiplied.  The 16-byte chunks of a row are stored at
 // (chunk ^ row % 8), so that 8 lanes that read one chunk of 8 rows meet different
-// banks.  A stage is two matrix steps; lane group g (16 lanes) takes chunks 2g and
-// 2g+1, which puts its two scales side by side in memory.  Fragments are read one step
-// ahead of the matrix instructions, so one barrier a stage is enough: after the first
-// step's instructions every wave holds the rest of the stage in registers, its LDS is
-// free for the stage after next, and the next stage has landed.
+// banks.  A stage is four matrix steps; lane half g takes chunks 4g to 4g+3, which puts
+// its four scales side by side in memory.  Fragments are read one step ahead of the
+// matrix instructions, so one barrier a stage is enough: before the last step every wave
+// holds the rest of the stage in registers, its LDS is free for the stage after next,
+// and the next stage has landed.
 //
 // Rows behind a segment, weight rows behind N and chunks behind H are loaded as zeros
 // by the range check of the buffer descriptors (their scales too, so a NaN scale of a
@@ -33,6 +33,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
@@ -40,7 +41,10 @@ constexpr int kBN = 256;          // weight rows of a tile
 constexpr int kStageChunks = 8;   // 16-byte chunks of a row in a stage: 256 codes
 constexpr int kStageBytes = 128;
 constexpr int kFp4 = 4;           // the matrix instruction's format code of e2m1
-constexpr uint32_t kOutside = 0xF0000000u;   // an offset past every descriptor's range
+
+// Ored to an offset below 2^31 it leaves every descriptor's range (2^31 at the most).
+// By arithmetic, not by a choice: a branch would split the blocks of the main loop.
+__device__ __forceinline__ uint32_t outside_if(bool b) { return (uint32_t)b << 31; }
 
 using Lds = __attribute__((address_space(3))) uint8_t;
 
@@ -49,6 +53,11 @@ struct Tile {
     int64_t row0;   // first row
     int rows;       // rows of it, at most BM
 };
+
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 | lo);
+}
 
 // Rows of expert e inside the buffer.
 __device__ __forceinline__ int segment(const ProductArgs& a, int e, int64_t& first) {
@@ -76,6 +85,7 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs& a, int64_t b, int c
     }
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) total += __shfl_xor(total, d);
+    total = __builtin_amdgcn_readfirstlane(total);
     const int64_t items = (int64_t)total * col_tiles;
     const int64_t per = (items + 7) / 8;
     const int64_t item = (int64_t)(b % 8) * per + b / 8;
@@ -123,9 +133,8 @@ __device__ __forceinline__ void stage8(__amdgpu_buffer_rsrc_t r, uint8_t* lds, u
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (Lds*)lds, 16, (int)off, 0, 0, 0);
 }
 
-template <bool F32>
-__device__ __forceinline__ void store4(void* y, int64_t at, f32x4 v) {
-    if constexpr (F32) {
+__device__ __forceinline__ void store4(void* y, bool f32, int64_t at, f32x4 v) {
+    if (f32) {
         *(f32x4*)((float*)y + at) = v;
     } else {
         *(u32x2*)((uint16_t*)y + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
@@ -138,17 +147,23 @@ __device__ __forceinline__ float silu_of(float g) {
 }
 
 // WM x WN waves: a wave owns BM / WM rows and kBN / WN weight rows.
-template <int BM, int WM, bool SWIGLU, bool F32>
+// WORDS: every row's scales start and end at a whole word.
+template <int BM, int WM, bool SWIGLU, bool WORDS>
 __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int col_tiles,
                                                               int64_t base) {
     constexpr int WN = kWaves / WM;
-    constexpr int MT = BM / WM / 16, NT = kBN / WN / 16;
+    constexpr int MT = BM / WM / 32, NT = kBN / WN / 32;
     constexpr int kLoadsA = BM / 8 / kWaves, kLoadsW = kBN / 8 / kWaves;
     __shared__ __align__(16) uint8_t lds_a0[BM * kStageBytes], lds_a1[BM * kStageBytes];
     __shared__ __align__(16) uint8_t lds_w0[kBN * kStageBytes], lds_w1[kBN * kStageBytes];
 
-    int col;
-    const Tile t = find_tile<BM>(a, base + blockIdx.x, col_tiles, col);
+    int col = 0;
+    Tile t = find_tile<BM>(a, base + blockIdx.x, col_tiles, col);
+    // the same in every lane: into scalar registers, where descriptors have to be
+    t.e = __builtin_amdgcn_readfirstlane(t.e);
+    t.row0 = uniform(t.row0);
+    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    col = __builtin_amdgcn_readfirstlane(col);
     if (t.e < 0) return;
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -170,134 +185,157 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
     const auto rsu = SWIGLU ? rows_of(a.w_scales, wrow + NO, wrows, nblk) : rsw;
 
     // Weight row (within its half) of tile row r.
-    auto weight_row = [](int r) { return SWIGLU ? (r >> 5) * 16 + (r & 15) : r; };
+    auto weight_row = [](int r) { return SWIGLU ? (r >> 6) * 32 + (r & 31) : r; };
 
+    static_assert(kLoadsW * 8 % 64 == 0, "a wave starts at a gate row");
     const int chunk = (lane % 8) ^ (lane / 8);
     auto load_stage = [&](uint8_t* la, uint8_t* lw, int s) {
         const uint32_t at = (uint32_t)(s * kStageChunks + chunk);
-        const bool in = (int)at < nblk;
+        const uint32_t bad = outside_if((int)at >= nblk);
 #pragma unroll
         for (int i = 0; i < kLoadsA; ++i) {
             const int r8 = (wave * kLoadsA + i) * 8;
-            const uint32_t off = in ? (uint32_t)(r8 + lane / 8) * (uint32_t)rb + at * 16 : kOutside;
-            stage8(ra, la + r8 * kStageBytes, off);
+            stage8(ra, la + r8 * kStageBytes, ((uint32_t)(r8 + lane / 8) * (uint32_t)rb + at * 16) | bad);
         }
 #pragma unroll
         for (int i = 0; i < kLoadsW; ++i) {
             const int r8 = (wave * kLoadsW + i) * 8;
             const int row = weight_row(r8) + lane / 8;
-            const uint32_t off = in ? (uint32_t)row * (uint32_t)rb + at * 16 : kOutside;
-            stage8(SWIGLU && (r8 & 16) ? ru : rw, lw + r8 * kStageBytes, off);
+            stage8(SWIGLU && (i * 8 & 32) ? ru : rw, lw + r8 * kStageBytes,
+                   ((uint32_t)row * (uint32_t)rb + at * 16) | bad);
         }
     };
 
-    const int r = lane % 16, g = lane / 16;
-    // The two scale bytes of a lane in stage s (byte i: matrix step i).
-    auto scale2 = [&](__amdgpu_buffer_rsrc_t rs, int row, int s) -> uint32_t {
-        const int b = s * kStageChunks + 2 * g;
+    const int r = lane % 32, g = lane / 32;
+    // The four scale bytes of a lane in stage s (byte i: matrix step i).
+    auto scale4 = [&](__amdgpu_buffer_rsrc_t rs, int row, int s) -> uint32_t {
+        const int b = s * kStageChunks + 4 * g;
         const uint32_t off = (uint32_t)row * (uint32_t)nblk + (uint32_t)b;
-        const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b8(rs, b < nblk ? (int)off : (int)kOutside, 0, 0);
-        const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b8(rs, b + 1 < nblk ? (int)off + 1 : (int)kOutside, 0, 0);
-        return lo | (hi << 8);
+        if constexpr (WORDS)
+            return __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(off | outside_if(b >= nblk)), 0, 0);
+        uint32_t v = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
+                     rs, (int)((off + i) | outside_if(b + i >= nblk)), 0, 0) << (8 * i);
+        return v;
     };
     uint32_t sw[2][NT], sa[2][MT];
     auto load_scales = [&](int which, int s) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int tr = wn * NT + i;
-            sw[which][i] = scale2(SWIGLU && (tr & 1) ? rsu : rsw, weight_row(tr * 16) + r, s);
+            sw[which][i] = scale4(SWIGLU && (tr & 1) ? rsu : rsw, weight_row(tr * 32) + r, s);
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i) sa[which][i] = scale2(rsa, (wm * MT + i) * 16 + r, s);
+        for (int i = 0; i < MT; ++i) sa[which][i] = scale4(rsa, (wm * MT + i) * 32 + r, s);
     };
 
     i32x8 fw[2][NT], fa[2][MT];
-    const uint32_t frag0 = (uint32_t)(r * kStageBytes + (((2 * g) ^ (r & 7)) * 16));
-    auto read_frags = [&](int step, const uint8_t* la, const uint8_t* lw) {
+    const uint32_t frag0 = (uint32_t)(r * kStageBytes + (((4 * g) ^ (r & 7)) * 16));
+    // The fragments of matrix step `step` into set `set`.
+    auto read_frags = [&](int set, int step, const uint8_t* la, const uint8_t* lw) {
         const uint32_t at = frag0 ^ (uint32_t)(step * 16);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            const u32x4 v = *(const u32x4*)(lw + (wn * NT + i) * 16 * kStageBytes + at);
-            fw[step][i] = i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+            const u32x4 v = *(const u32x4*)(lw + (wn * NT + i) * 32 * kStageBytes + at);
+            fw[set][i] = i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            const u32x4 v = *(const u32x4*)(la + (wm * MT + i) * 16 * kStageBytes + at);
-            fa[step][i] = i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+            const u32x4 v = *(const u32x4*)(la + (wm * MT + i) * 32 * kStageBytes + at);
+            fa[set][i] = i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
         }
     };
 
-    f32x4 acc[NT][MT];
+    f32x16 acc[NT][MT];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
 
-#define MOE_MX_STEP(STEP, SET)                                                              \
+// The order of loads and matrix instructions stays as written from step to step.
+#define MOE_MX_STEP(FRAGS, STEP, SET)                                                       \
     _Pragma("unroll") for (int i = 0; i < NT; ++i)                                          \
         _Pragma("unroll") for (int j = 0; j < MT; ++j)                                      \
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(                   \
-                fw[STEP][i], fa[STEP][j], acc[i][j], kFp4, kFp4, STEP, (int)sw[SET][i],     \
-                STEP, (int)sa[SET][j])
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                    \
+                fw[FRAGS][i], fa[FRAGS][j], acc[i][j], kFp4, kFp4, STEP, (int)sw[SET][i],   \
+                STEP, (int)sa[SET][j]);                                                     \
+    __builtin_amdgcn_sched_barrier(0)
 
     // Every wave's loads into LDS have landed and every wave's reads are in registers.
     auto sync_stage = [] {
         __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
     };
+// Stage s in LDS buffers A, W and scale set SET, its first fragments already read; the
+// next stage is on its way into NA, NW.
+#define MOE_MX_STAGE(A, W, NA, NW, SET)   \
+    read_frags(1, 1, A, W);               \
+    MOE_MX_STEP(0, 0, SET);               \
+    read_frags(0, 2, A, W);               \
+    MOE_MX_STEP(1, 1, SET);               \
+    read_frags(1, 3, A, W);               \
+    MOE_MX_STEP(0, 2, SET);               \
+    sync_stage();                         \
+    load_stage(A, W, s + 2);              \
+    read_frags(0, 0, NA, NW);             \
+    MOE_MX_STEP(1, 3, SET);               \
+    load_scales(SET, s + 2);              \
+    ++s
+
     load_stage(lds_a0, lds_w0, 0);
     load_scales(0, 0);
     sync_stage();
     load_stage(lds_a1, lds_w1, 1);      // past the last stage: zeros
     load_scales(1, 1);
-    read_frags(0, lds_a0, lds_w0);
+    read_frags(0, 0, lds_a0, lds_w0);
     int s = 0;
-    for (; s + 1 < stages; s += 2) {
-        read_frags(1, lds_a0, lds_w0);
-        MOE_MX_STEP(0, 0);
-        sync_stage();
-        load_stage(lds_a0, lds_w0, s + 2);
-        read_frags(0, lds_a1, lds_w1);
-        MOE_MX_STEP(1, 0);
-        load_scales(0, s + 2);
-        read_frags(1, lds_a1, lds_w1);
-        MOE_MX_STEP(0, 1);
-        sync_stage();
-        load_stage(lds_a1, lds_w1, s + 3);
-        read_frags(0, lds_a0, lds_w0);
-        MOE_MX_STEP(1, 1);
-        load_scales(1, s + 3);
+    while (s + 1 < stages) {
+        MOE_MX_STAGE(lds_a0, lds_w0, lds_a1, lds_w1, 0);
+        MOE_MX_STAGE(lds_a1, lds_w1, lds_a0, lds_w0, 1);
     }
     if (s < stages) {
-        read_frags(1, lds_a0, lds_w0);
-        MOE_MX_STEP(0, 0);
-        MOE_MX_STEP(1, 0);
+        MOE_MX_STAGE(lds_a0, lds_w0, lds_a1, lds_w1, 0);
     }
+#undef MOE_MX_STAGE
 #undef MOE_MX_STEP
     // no load into LDS may be in flight when the workgroup's LDS goes to the next one
     __builtin_amdgcn_s_waitcnt(0);
 
+    // a lane holds columns r of the tile (a row of y) and weight rows 8 * p + 4 * g + 0..3
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
-        const int row = (wm * MT + j) * 16 + r;
+        const int row = (wm * MT + j) * 32 + r;
         if (row >= t.rows) continue;
         const int64_t out = (t.row0 + row) * NO;
         if constexpr (SWIGLU) {
 #pragma unroll
-            for (int i = 0; i < NT; i += 2) {
-                const int64_t n = n0 + (wn * NT + i) / 2 * 16 + g * 4;
-                if (n >= NO) continue;
-                f32x4 v;
+            for (int i = 0; i < NT; i += 2)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = silu_of(acc[i][j][q]) * acc[i + 1][j][q];
-                store4<F32>(a.y, out + n, v);
-            }
+                for (int p = 0; p < 4; ++p) {
+                    const int64_t n = n0 + (wn * NT + i) / 2 * 32 + 8 * p + 4 * g;
+                    if (n >= NO) continue;
+                    f32x4 v;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        v[q] = silu_of(acc[i][j][4 * p + q]) * acc[i + 1][j][4 * p + q];
+                    store4(a.y, a.y_f32, out + n, v);
+                }
         } else {
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int64_t n = n0 + (wn * NT + i) * 16 + g * 4;
-                if (n < NO) store4<F32>(a.y, out + n, acc[i][j]);
-            }
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const int64_t n = n0 + (wn * NT + i) * 32 + 8 * p + 4 * g;
+                    if (n >= NO) continue;
+                    const f32x4 v = {acc[i][j][4 * p], acc[i][j][4 * p + 1], acc[i][j][4 * p + 2],
+                                     acc[i][j][4 * p + 3]};
+                    store4(a.y, a.y_f32, out + n, v);
+                }
         }
     }
 }
@@ -306,16 +344,17 @@ template <int BM, int WM>
 hipError_t launch(const ProductArgs& a, hipStream_t s) {
     const int64_t cols = a.swiglu ? a.N / 2 : a.N;
     const int col_tiles = (int)((cols + (a.swiglu ? kBN / 2 : kBN) - 1) / (a.swiglu ? kBN / 2 : kBN));
+    const bool words = a.H / kMxBlock % 4 == 0 && ((uintptr_t)a.a_scales | (uintptr_t)a.w_scales) % 4 == 0;
     // every expert may have one tile that is not full
     const int64_t row_tiles = a.rows / BM + (a.E < a.rows ? a.E : a.rows);
     const int64_t blocks = (row_tiles * col_tiles + 7) / 8 * 8;
     for (int64_t base = 0; base < blocks; base += kMaxGrid) {
         const dim3 grid((unsigned)(blocks - base < kMaxGrid ? blocks - base : kMaxGrid));
         if (a.swiglu) {
-            if (a.y_f32) product_kernel<BM, WM, true, true><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
+            if (words) product_kernel<BM, WM, true, true><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
             else product_kernel<BM, WM, true, false><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
         } else {
-            if (a.y_f32) product_kernel<BM, WM, false, true><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
+            if (words) product_kernel<BM, WM, false, true><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
             else product_kernel<BM, WM, false, false><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
         }
     }

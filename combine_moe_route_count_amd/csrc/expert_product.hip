@@ -24,6 +24,8 @@
 // Rows behind a segment, weight rows behind N and chunks behind H are loaded as zeros
 // by the range check of the buffer descriptors (their scales too, so a NaN scale of a
 // neighbour does not get in); they are never stored.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "experts.hpp"
 
@@ -40,10 +42,11 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kBN = 256;          // weight rows of a tile
 constexpr int kStageChunks = 8;   // 16-byte chunks of a row in a stage: 256 codes
 constexpr int kStageBytes = 128;
+constexpr int kGroup = 4;         // stages whose scales are loaded together
+constexpr int kGroupChunks = kGroup * kStageChunks;
 constexpr int kFp4 = 4;           // the matrix instruction's format code of e2m1
 
 // Ored to an offset below 2^31 it leaves every descriptor's range (2^31 at the most).
-// By arithmetic, not by a choice: a branch would split the blocks of the main loop.
 __device__ __forceinline__ uint32_t outside_if(bool b) { return (uint32_t)b << 31; }
 
 using Lds = __attribute__((address_space(3))) uint8_t;
@@ -171,6 +174,7 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
     const int64_t rb = a.H / 2;            // bytes of a row of codes
     const int nblk = (int)(a.H / kMxBlock);
     const int stages = (nblk + kStageChunks - 1) / kStageChunks;
+    const int whole_stages = WORDS && BM > 32 ? nblk / kGroupChunks * kGroup : 0;
     const int64_t NO = SWIGLU ? a.N / 2 : a.N;     // output columns
     const int64_t n0 = (int64_t)col * (SWIGLU ? kBN / 2 : kBN);
     const int64_t wrow = (int64_t)t.e * a.N + n0;
@@ -189,8 +193,13 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
 
     static_assert(kLoadsW * 8 % 64 == 0, "a wave starts at a gate row");
     const int chunk = (lane % 8) ^ (lane / 8);
+    const int spread = chunk % 4 + (chunk / 4) * (kGroupChunks / 2);
     auto load_stage = [&](uint8_t* la, uint8_t* lw, int s) {
-        const uint32_t at = (uint32_t)(s * kStageChunks + chunk);
+        // all by arithmetic: a branch would split the blocks of the main loop
+        const int whole = (s - whole_stages) >> 31;     // -1: yes, 0: no
+        const int group = s / kGroup * kGroupChunks + s % kGroup * 4;
+        const int first = s * kStageChunks + ((group - s * kStageChunks) & whole);
+        const uint32_t at = (uint32_t)(first + chunk + ((spread - chunk) & whole));
         const uint32_t bad = outside_if((int)at >= nblk);
 #pragma unroll
         for (int i = 0; i < kLoadsA; ++i) {
@@ -207,28 +216,51 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
     };
 
     const int r = lane % 32, g = lane / 32;
-    // The four scale bytes of a lane in stage s (byte i: matrix step i).
-    auto scale4 = [&](__amdgpu_buffer_rsrc_t rs, int row, int s) -> uint32_t {
-        const int b = s * kStageChunks + 4 * g;
-        const uint32_t off = (uint32_t)row * (uint32_t)nblk + (uint32_t)b;
-        if constexpr (WORDS)
-            return __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(off | outside_if(b >= nblk)), 0, 0);
-        uint32_t v = 0;
+    // The scale bytes of a lane in a group of stages: byte j of word i is that of matrix
+    // step j of stage i.
+    auto scale16 = [&](__amdgpu_buffer_rsrc_t rs, int row, int group, auto whole) -> u32x4 {
+        const uint32_t off = (uint32_t)row * (uint32_t)nblk + (uint32_t)(group * kGroupChunks);
+        u32x4 v;
+        if constexpr (decltype(whole)::value) {
+            v = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(off + (kGroupChunks / 2) * g), 0, 0);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
-                     rs, (int)((off + i) | outside_if(b + i >= nblk)), 0, 0) << (8 * i);
+            for (int i = 0; i < kGroup; ++i) {
+                const int b = i * kStageChunks + 4 * g;
+                const int room = nblk - group * kGroupChunks - b;   // blocks from there on
+                if constexpr (WORDS) {
+                    v[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)((off + b) | outside_if(room <= 0)), 0, 0);
+                } else {
+                    uint32_t w = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
+                                 rs, (int)((off + b + j) | outside_if(room <= j)), 0, 0) << (8 * j);
+                    v[i] = w;
+                }
+            }
+        }
         return v;
     };
-    uint32_t sw[2][NT], sa[2][MT];
-    auto load_scales = [&](int which, int s) {
+    u32x4 sw[NT], sa[MT], next_sw[NT], next_sa[MT];
+    auto load_group = [&](int group, auto whole) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int tr = wn * NT + i;
-            sw[which][i] = scale4(SWIGLU && (tr & 1) ? rsu : rsw, weight_row(tr * 32) + r, s);
+            next_sw[i] = scale16(SWIGLU && (i & 1) ? rsu : rsw, weight_row(tr * 32) + r, group, whole);
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i) sa[which][i] = scale4(rsa, (wm * MT + i) * 32 + r, s);
+        for (int i = 0; i < MT; ++i) next_sa[i] = scale16(rsa, (wm * MT + i) * 32 + r, group, whole);
+    };
+    auto load_scales = [&](int group) {
+        if (WORDS && BM > 32 && group * kGroup < whole_stages) load_group(group, std::true_type{});
+        else load_group(group, std::false_type{});
+    };
+    auto take_scales = [&] {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) sw[i] = next_sw[i];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) sa[i] = next_sa[i];
     };
 
     i32x8 fw[2][NT], fa[2][MT];
@@ -257,12 +289,16 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
             for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
 
 // The order of loads and matrix instructions stays as written from step to step.
-#define MOE_MX_STEP(FRAGS, STEP, SET)                                                       \
+#define MOE_MX_STEP(FRAGS, STEP, STAGE)                                                       \
     _Pragma("unroll") for (int i = 0; i < NT; ++i)                                          \
         _Pragma("unroll") for (int j = 0; j < MT; ++j)                                      \
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                    \
-                fw[FRAGS][i], fa[FRAGS][j], acc[i][j], kFp4, kFp4, STEP, (int)sw[SET][i],   \
-                STEP, (int)sa[SET][j]);                                                     \
+                fw[FRAGS][i], fa[FRAGS][j], acc[i][j], kFp4, kFp4, STEP, (int)sw[i][STAGE], \
+                STEP, (int)sa[j][STAGE]);                                                    \
+    _Pragma("unroll") for (int i = 0; i < NT + MT; ++i) {                                   \
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0); /* one LDS read */               \
+        __builtin_amdgcn_sched_group_barrier(0x008, NT * MT / (NT + MT), 0);                \
+    }                                                                                       \
     __builtin_amdgcn_sched_barrier(0)
 
     // Every wave's loads into LDS have landed and every wave's reads are in registers.
@@ -271,35 +307,44 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
     };
-// Stage s in LDS buffers A, W and scale set SET, its first fragments already read; the
-// next stage is on its way into NA, NW.
-#define MOE_MX_STAGE(A, W, NA, NW, SET)   \
+// Stage s, number STAGE of its group, in LDS buffers A, W, its first fragments already
+// read; the next stage is on its way into NA, NW.
+#define MOE_MX_STAGE(A, W, NA, NW, STAGE) \
     read_frags(1, 1, A, W);               \
-    MOE_MX_STEP(0, 0, SET);               \
+    MOE_MX_STEP(0, 0, STAGE);             \
     read_frags(0, 2, A, W);               \
-    MOE_MX_STEP(1, 1, SET);               \
+    MOE_MX_STEP(1, 1, STAGE);             \
     read_frags(1, 3, A, W);               \
-    MOE_MX_STEP(0, 2, SET);               \
+    MOE_MX_STEP(0, 2, STAGE);             \
     sync_stage();                         \
     load_stage(A, W, s + 2);              \
     read_frags(0, 0, NA, NW);             \
-    MOE_MX_STEP(1, 3, SET);               \
-    load_scales(SET, s + 2);              \
+    MOE_MX_STEP(1, 3, STAGE);             \
     ++s
 
     load_stage(lds_a0, lds_w0, 0);
-    load_scales(0, 0);
+    load_scales(0);
     sync_stage();
     load_stage(lds_a1, lds_w1, 1);      // past the last stage: zeros
-    load_scales(1, 1);
     read_frags(0, 0, lds_a0, lds_w0);
     int s = 0;
-    while (s + 1 < stages) {
+    while (s + kGroup <= stages) {
+        take_scales();
+        load_scales(s / kGroup + 1);
         MOE_MX_STAGE(lds_a0, lds_w0, lds_a1, lds_w1, 0);
+        MOE_MX_STAGE(lds_a1, lds_w1, lds_a0, lds_w0, 1);
+        MOE_MX_STAGE(lds_a0, lds_w0, lds_a1, lds_w1, 2);
+        MOE_MX_STAGE(lds_a1, lds_w1, lds_a0, lds_w0, 3);
+    }
+    take_scales();
+    if (s < stages) {
+        MOE_MX_STAGE(lds_a0, lds_w0, lds_a1, lds_w1, 0);
+    }
+    if (s < stages) {
         MOE_MX_STAGE(lds_a1, lds_w1, lds_a0, lds_w0, 1);
     }
     if (s < stages) {
-        MOE_MX_STAGE(lds_a0, lds_w0, lds_a1, lds_w1, 0);
+        MOE_MX_STAGE(lds_a0, lds_w0, lds_a1, lds_w1, 2);
     }
 #undef MOE_MX_STAGE
 #undef MOE_MX_STEP

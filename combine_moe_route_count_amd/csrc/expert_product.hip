@@ -40,14 +40,16 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kBN = 256;          // weight rows of a tile
-constexpr int kStageChunks = 8;   // 16-byte chunks of a row in a stage: 256 codes
-constexpr int kStageBytes = 128;
-constexpr int kGroup = 4;         // stages whose scales are loaded together
+constexpr int kStageChunks = 4;   // 16-byte chunks of a row in a stage: 128 codes
+constexpr int kStageBytes = 64;
+constexpr int kGroup = 4;         // stages in LDS, and stages whose scales are loaded together
 constexpr int kGroupChunks = kGroup * kStageChunks;
 constexpr int kFp4 = 4;           // the matrix instruction's format code of e2m1
 
 // Ored to an offset below 2^31 it leaves every descriptor's range (2^31 at the most).
 __device__ __forceinline__ uint32_t outside_if(bool b) { return (uint32_t)b << 31; }
+
+constexpr int kRowGroup = 4;       // row tiles of an expert that are worked on side by side
 
 using Lds = __attribute__((address_space(3))) uint8_t;
 
@@ -72,10 +74,11 @@ __device__ __forceinline__ int segment(const ProductArgs& a, int e, int64_t& fir
     return hi > first ? (int)(hi - first) : 0;
 }
 
-// The row tile that workgroup b works on: experts in order, BM rows at a time.  Row
-// tiles times column tiles are dealt out so that each XCD (workgroups go to them in
-// turn) gets one run of neighbours, which share weights and rows in its L2.  Every
-// wave finds the tile by itself, 64 experts at a time.
+// The tile that workgroup b works on.  Experts in order; of one expert, kRowGroup row tiles
+// at a time, row tiles first, so that tiles that run together share few weight rows and
+// few token rows.  The sequence is cut into 8 runs, one for each XCD (workgroups go to
+// them in turn), so that neighbours share an L2.  Every wave finds the tile by itself, 64
+// experts at a time.
 template <int BM>
 __device__ __forceinline__ Tile find_tile(const ProductArgs& a, int64_t b, int col_tiles,
                                           int& col) {
@@ -94,26 +97,32 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs& a, int64_t b, int c
     const int64_t item = (int64_t)(b % 8) * per + b / 8;
     Tile t{-1, 0, 0};
     if (b / 8 >= per || item >= items) return t;
-    int at = (int)(item / col_tiles);
-    col = (int)(item - (int64_t)at * col_tiles);
+    const int at = (int)(item / col_tiles);    // row tile, if an expert's were not grouped
+    int before = 0;                            // row tiles of the experts looked at
     for (int e0 = 0; e0 < a.E; e0 += kWave) {
         int64_t first = 0;
         const int n = e0 + lane < a.E ? segment(a, e0 + lane, first) : 0;
         const int mine = (n + BM - 1) / BM;
-        int upto = mine;   // tiles of the experts up to and with this lane's
+        int upto = mine;   // row tiles of the experts up to and with this lane's
 #pragma unroll
         for (int d = 1; d < kWave; d *= 2) {
             const int o = __shfl_up(upto, d);
             if (lane >= d) upto += o;
         }
         const int here = readlane(upto, kWave - 1);
-        if (at >= here) {
-            at -= here;
+        if (at - before >= here) {
+            before += here;
             continue;
         }
-        const int owner = __builtin_ctzll(ballot64(upto > at));
-        const int skip = at - (readlane(upto, owner) - readlane(mine, owner));
-        const int cnt = readlane(n, owner);
+        const int owner = __builtin_ctzll(ballot64(upto > at - before));
+        const int tiles = readlane(mine, owner), cnt = readlane(n, owner);
+        before += readlane(upto, owner) - tiles;
+        const int64_t local = item - (int64_t)before * col_tiles;
+        const int top = (int)(local / ((int64_t)kRowGroup * col_tiles)) * kRowGroup;
+        const int rows = tiles - top < kRowGroup ? tiles - top : kRowGroup;
+        const int in_group = (int)(local - (int64_t)top * col_tiles);
+        col = in_group / rows;
+        const int skip = top + in_group - col * rows;
         const uint64_t f = (uint64_t)first;
         const int64_t start = (int64_t)(((uint64_t)(uint32_t)readlane((int)(f >> 32), owner) << 32) |
                                         (uint32_t)readlane((int)f, owner));
@@ -131,8 +140,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const uint8_t* base, i
                                              (int)(uint32_t)(rows * row_bytes), kRsrcWord3);
 }
 
-// 8 rows of a stage into LDS: lane l fetches chunk (l % 8) ^ (l / 8) of row l / 8.
-__device__ __forceinline__ void stage8(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off) {
+// 16 rows of a stage into LDS, lane l's 16 bytes to l * 16.
+__device__ __forceinline__ void stage16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (Lds*)lds, 16, (int)off, 0, 0, 0);
 }
 
@@ -156,9 +165,10 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
                                                               int64_t base) {
     constexpr int WN = kWaves / WM;
     constexpr int MT = BM / WM / 32, NT = kBN / WN / 32;
-    constexpr int kLoadsA = BM / 8 / kWaves, kLoadsW = kBN / 8 / kWaves;
-    __shared__ __align__(16) uint8_t lds_a0[BM * kStageBytes], lds_a1[BM * kStageBytes];
-    __shared__ __align__(16) uint8_t lds_w0[kBN * kStageBytes], lds_w1[kBN * kStageBytes];
+    constexpr int kLoadsA = (BM / 16 + kWaves - 1) / kWaves, kLoadsW = kBN / 16 / kWaves;
+    constexpr int kA = BM * kStageBytes;     // where a stage's weight rows begin
+    __shared__ __align__(16) uint8_t lds0[kA + kBN * kStageBytes], lds1[kA + kBN * kStageBytes];
+    __shared__ __align__(16) uint8_t lds2[kA + kBN * kStageBytes], lds3[kA + kBN * kStageBytes];
 
     int col = 0;
     Tile t = find_tile<BM>(a, base + blockIdx.x, col_tiles, col);
@@ -174,7 +184,6 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
     const int64_t rb = a.H / 2;            // bytes of a row of codes
     const int nblk = (int)(a.H / kMxBlock);
     const int stages = (nblk + kStageChunks - 1) / kStageChunks;
-    const int whole_stages = WORDS && BM > 32 ? nblk / kGroupChunks * kGroup : 0;
     const int64_t NO = SWIGLU ? a.N / 2 : a.N;     // output columns
     const int64_t n0 = (int64_t)col * (SWIGLU ? kBN / 2 : kBN);
     const int64_t wrow = (int64_t)t.e * a.N + n0;
@@ -191,92 +200,96 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
     // Weight row (within its half) of tile row r.
     auto weight_row = [](int r) { return SWIGLU ? (r >> 6) * 32 + (r & 31) : r; };
 
-    static_assert(kLoadsW * 8 % 64 == 0, "a wave starts at a gate row");
-    const int chunk = (lane % 8) ^ (lane / 8);
-    const int spread = chunk % 4 + (chunk / 4) * (kGroupChunks / 2);
-    auto load_stage = [&](uint8_t* la, uint8_t* lw, int s) {
-        // all by arithmetic: a branch would split the blocks of the main loop
-        const int whole = (s - whole_stages) >> 31;     // -1: yes, 0: no
-        const int group = s / kGroup * kGroupChunks + s % kGroup * 4;
-        const int first = s * kStageChunks + ((group - s * kStageChunks) & whole);
-        const uint32_t at = (uint32_t)(first + chunk + ((spread - chunk) & whole));
+    static_assert(kLoadsW * 16 % 64 == 0, "a wave starts at a gate row");
+    const int chunk = (lane % 4) ^ (lane / 8 % 4);
+    auto load_stage = [&](uint8_t* lds, int s) {
+        const uint32_t at = (uint32_t)(s * kStageChunks + chunk);
         const uint32_t bad = outside_if((int)at >= nblk);
 #pragma unroll
         for (int i = 0; i < kLoadsA; ++i) {
-            const int r8 = (wave * kLoadsA + i) * 8;
-            stage8(ra, la + r8 * kStageBytes, ((uint32_t)(r8 + lane / 8) * (uint32_t)rb + at * 16) | bad);
+            // 32 rows are two loads for four waves: two waves each fetch the same
+            const int r16 = (wave * kLoadsA + i) * 16 % BM;
+            stage16(ra, lds + r16 * kStageBytes,
+                    ((uint32_t)(r16 + lane / 4) * (uint32_t)rb + at * 16) | bad);
         }
 #pragma unroll
         for (int i = 0; i < kLoadsW; ++i) {
-            const int r8 = (wave * kLoadsW + i) * 8;
-            const int row = weight_row(r8) + lane / 8;
-            stage8(SWIGLU && (i * 8 & 32) ? ru : rw, lw + r8 * kStageBytes,
-                   ((uint32_t)row * (uint32_t)rb + at * 16) | bad);
+            const int r16 = (wave * kLoadsW + i) * 16;
+            const int row = weight_row(r16) + lane / 4;
+            stage16(SWIGLU && (i * 16 & 32) ? ru : rw, lds + kA + r16 * kStageBytes,
+                    ((uint32_t)row * (uint32_t)rb + at * 16) | bad);
         }
     };
 
     const int r = lane % 32, g = lane / 32;
-    // The scale bytes of a lane in a group of stages: byte j of word i is that of matrix
-    // step j of stage i.
+    // The scales of a lane's row in a group of stages: bytes 2g and 2g + 1 of word i are
+    // those of the two matrix steps of stage i.
     auto scale16 = [&](__amdgpu_buffer_rsrc_t rs, int row, int group, auto whole) -> u32x4 {
         const uint32_t off = (uint32_t)row * (uint32_t)nblk + (uint32_t)(group * kGroupChunks);
         u32x4 v;
         if constexpr (decltype(whole)::value) {
-            v = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(off + (kGroupChunks / 2) * g), 0, 0);
+            v = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off, 0, 0);
         } else {
 #pragma unroll
             for (int i = 0; i < kGroup; ++i) {
-                const int b = i * kStageChunks + 4 * g;
-                const int room = nblk - group * kGroupChunks - b;   // blocks from there on
+                const int room = nblk - group * kGroupChunks - i * kStageChunks;   // blocks from there on
                 if constexpr (WORDS) {
-                    v[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)((off + b) | outside_if(room <= 0)), 0, 0);
+                    v[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)((off + 4 * i) | outside_if(room <= 0)), 0, 0);
                 } else {
                     uint32_t w = 0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 2; ++j)
                         w |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
-                                 rs, (int)((off + b + j) | outside_if(room <= j)), 0, 0) << (8 * j);
-                    v[i] = w;
+                                 rs, (int)((off + 4 * i + 2 * g + j) | outside_if(room <= 2 * g + j)), 0, 0)
+                             << (8 * j);
+                    v[i] = w << (16 * g);
                 }
             }
         }
         return v;
     };
-    u32x4 sw[NT], sa[MT], next_sw[NT], next_sa[MT];
+    u32x4 qw[NT], qa[MT], next_qw[NT], next_qa[MT];
     auto load_group = [&](int group, auto whole) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int tr = wn * NT + i;
-            next_sw[i] = scale16(SWIGLU && (i & 1) ? rsu : rsw, weight_row(tr * 32) + r, group, whole);
+            next_qw[i] = scale16(SWIGLU && (i & 1) ? rsu : rsw, weight_row(tr * 32) + r, group, whole);
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i) next_sa[i] = scale16(rsa, (wm * MT + i) * 32 + r, group, whole);
+        for (int i = 0; i < MT; ++i) next_qa[i] = scale16(rsa, (wm * MT + i) * 32 + r, group, whole);
     };
     auto load_scales = [&](int group) {
-        if (WORDS && BM > 32 && group * kGroup < whole_stages) load_group(group, std::true_type{});
+        if (WORDS && (group + 1) * kGroupChunks <= nblk) load_group(group, std::true_type{});
         else load_group(group, std::false_type{});
     };
     auto take_scales = [&] {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) sw[i] = next_sw[i];
+        for (int i = 0; i < NT; ++i) qw[i] = next_qw[i];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) sa[i] = next_sa[i];
+        for (int i = 0; i < MT; ++i) qa[i] = next_qa[i];
+    };
+    uint32_t sw[NT], sa[MT];      // of one stage: bytes 0 and 1
+    auto stage_scales = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sw[j] = qw[j][i] >> (16 * g);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) sa[j] = qa[j][i] >> (16 * g);
     };
 
     i32x8 fw[2][NT], fa[2][MT];
-    const uint32_t frag0 = (uint32_t)(r * kStageBytes + (((4 * g) ^ (r & 7)) * 16));
-    // The fragments of matrix step `step` into set `set`.
-    auto read_frags = [&](int set, int step, const uint8_t* la, const uint8_t* lw) {
+    const uint32_t frag0 = (uint32_t)(r * kStageBytes + (((2 * g) ^ (r / 2 & 3)) * 16));
+    // The fragments of matrix step `step` into set `step`.
+    auto read_frags = [&](int step, const uint8_t* lds) {
         const uint32_t at = frag0 ^ (uint32_t)(step * 16);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            const u32x4 v = *(const u32x4*)(lw + (wn * NT + i) * 32 * kStageBytes + at);
-            fw[set][i] = i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+            const u32x4 v = *(const u32x4*)(lds + kA + (wn * NT + i) * 32 * kStageBytes + at);
+            fw[step][i] = i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            const u32x4 v = *(const u32x4*)(la + (wm * MT + i) * 32 * kStageBytes + at);
-            fa[set][i] = i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+            const u32x4 v = *(const u32x4*)(lds + (wm * MT + i) * 32 * kStageBytes + at);
+            fa[step][i] = i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
         }
     };
 
@@ -288,63 +301,73 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
 
-// The order of loads and matrix instructions stays as written from step to step.
-#define MOE_MX_STEP(FRAGS, STEP, STAGE)                                                       \
+// The order of loads and matrix instructions stays as written from step to step, LDS
+// reads spread over the matrix instructions.
+#define MOE_MX_STEP(STEP)                                                                   \
     _Pragma("unroll") for (int i = 0; i < NT; ++i)                                          \
         _Pragma("unroll") for (int j = 0; j < MT; ++j)                                      \
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                    \
-                fw[FRAGS][i], fa[FRAGS][j], acc[i][j], kFp4, kFp4, STEP, (int)sw[i][STAGE], \
-                STEP, (int)sa[j][STAGE]);                                                    \
+                fw[STEP][i], fa[STEP][j], acc[i][j], kFp4, kFp4, STEP, (int)sw[i], STEP,    \
+                (int)sa[j]);                                                                \
     _Pragma("unroll") for (int i = 0; i < NT + MT; ++i) {                                   \
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0); /* one LDS read */               \
         __builtin_amdgcn_sched_group_barrier(0x008, NT * MT / (NT + MT), 0);                \
     }                                                                                       \
     __builtin_amdgcn_sched_barrier(0)
 
-    // Every wave's loads into LDS have landed and every wave's reads are in registers.
-    auto sync_stage = [] {
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
+    // All but the last `flying` loads of every wave have landed, and every wave's LDS reads
+    // are in registers.  The empty asm keeps the compiler from moving memory accesses over
+    // the barrier.
+    auto sync = [](auto flying) {
+        constexpr int N = decltype(flying)::value;
+        static_assert(N < 64, "vmcnt");
+        asm volatile("" ::: "memory");
+        // simm16 of s_waitcnt: vmcnt in bits 3:0 and 15:14, expcnt 6:4 (none), lgkmcnt 11:8 (0)
+        __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x70);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
-// Stage s, number STAGE of its group, in LDS buffers A, W, its first fragments already
-// read; the next stage is on its way into NA, NW.
-#define MOE_MX_STAGE(A, W, NA, NW, STAGE) \
-    read_frags(1, 1, A, W);               \
-    MOE_MX_STEP(0, 0, STAGE);             \
-    read_frags(0, 2, A, W);               \
-    MOE_MX_STEP(1, 1, STAGE);             \
-    read_frags(1, 3, A, W);               \
-    MOE_MX_STEP(0, 2, STAGE);             \
-    sync_stage();                         \
-    load_stage(A, W, s + 2);              \
-    read_frags(0, 0, NA, NW);             \
-    MOE_MX_STEP(1, 3, STAGE);             \
+    constexpr int kLoads = kLoadsA + kLoadsW;    // of a wave for a stage
+// Stage s, number I of its group, in LDS buffer LDS, its first fragments already read; the
+// next stage is in NEXT, or on its way.
+#define MOE_MX_STAGE(LDS, NEXT, I) \
+    stage_scales(I);               \
+    read_frags(1, LDS);            \
+    MOE_MX_STEP(0);                \
+    sync(two_stages);              \
+    load_stage(LDS, s + kGroup);   \
+    read_frags(0, NEXT);           \
+    MOE_MX_STEP(1);                \
     ++s
 
-    load_stage(lds_a0, lds_w0, 0);
     load_scales(0);
-    sync_stage();
-    load_stage(lds_a1, lds_w1, 1);      // past the last stage: zeros
-    read_frags(0, 0, lds_a0, lds_w0);
+    load_stage(lds0, 0);
+    load_stage(lds1, 1);      // past the last stage: zeros
+    load_stage(lds2, 2);
+    load_stage(lds3, 3);
+    // stages s + 2 and s + 3 may be in flight when s + 1 has to be there
+    constexpr std::integral_constant<int, 2 * kLoads> two_stages{};
     int s = 0;
+    sync(std::integral_constant<int, 3 * kLoads>{});
+    read_frags(0, lds0);
     while (s + kGroup <= stages) {
         take_scales();
         load_scales(s / kGroup + 1);
-        MOE_MX_STAGE(lds_a0, lds_w0, lds_a1, lds_w1, 0);
-        MOE_MX_STAGE(lds_a1, lds_w1, lds_a0, lds_w0, 1);
-        MOE_MX_STAGE(lds_a0, lds_w0, lds_a1, lds_w1, 2);
-        MOE_MX_STAGE(lds_a1, lds_w1, lds_a0, lds_w0, 3);
+        MOE_MX_STAGE(lds0, lds1, 0);
+        MOE_MX_STAGE(lds1, lds2, 1);
+        MOE_MX_STAGE(lds2, lds3, 2);
+        MOE_MX_STAGE(lds3, lds0, 3);
     }
     take_scales();
     if (s < stages) {
-        MOE_MX_STAGE(lds_a0, lds_w0, lds_a1, lds_w1, 0);
+        MOE_MX_STAGE(lds0, lds1, 0);
     }
     if (s < stages) {
-        MOE_MX_STAGE(lds_a1, lds_w1, lds_a0, lds_w0, 1);
+        MOE_MX_STAGE(lds1, lds2, 1);
     }
     if (s < stages) {
-        MOE_MX_STAGE(lds_a0, lds_w0, lds_a1, lds_w1, 2);
+        MOE_MX_STAGE(lds2, lds3, 2);
     }
 #undef MOE_MX_STAGE
 #undef MOE_MX_STEP

@@ -145,14 +145,6 @@ __device__ __forceinline__ void stage16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, 
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (Lds*)lds, 16, (int)off, 0, 0, 0);
 }
 
-__device__ __forceinline__ void store4(void* y, bool f32, int64_t at, f32x4 v) {
-    if (f32) {
-        *(f32x4*)((float*)y + at) = v;
-    } else {
-        *(u32x2*)((uint16_t*)y + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-    }
-}
-
 __device__ __forceinline__ float silu_of(float g) {
     // g / (1 + exp(-g)); exp overflows to an infinity below -88, where the quotient is -0
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
@@ -223,46 +215,55 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
 
     const int r = lane % 32, g = lane / 32;
     // The scales of a lane's row in a group of stages: bytes 2g and 2g + 1 of word i are
-    // those of the two matrix steps of stage i.
-    auto scale16 = [&](__amdgpu_buffer_rsrc_t rs, int row, int group, auto whole) -> u32x4 {
+    // those of the two matrix steps of stage i.  Whole groups are loaded in pairs, 32 bytes
+    // of a row by two lanes, and taken apart when they are needed.
+    auto scale_pair = [&](__amdgpu_buffer_rsrc_t rs, int row, int group) -> u32x4 {
+        return __builtin_amdgcn_raw_buffer_load_b128(rs, row * nblk + (group + g) * kGroupChunks, 0, 0);
+    };
+    auto scale_rest = [&](__amdgpu_buffer_rsrc_t rs, int row, int group) -> u32x4 {
         const uint32_t off = (uint32_t)row * (uint32_t)nblk + (uint32_t)(group * kGroupChunks);
         u32x4 v;
-        if constexpr (decltype(whole)::value) {
-            v = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off, 0, 0);
-        } else {
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) {
-                const int room = nblk - group * kGroupChunks - i * kStageChunks;   // blocks from there on
-                if constexpr (WORDS) {
-                    v[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)((off + 4 * i) | outside_if(room <= 0)), 0, 0);
-                } else {
-                    uint32_t w = 0;
+        for (int i = 0; i < kGroup; ++i) {
+            const int room = nblk - group * kGroupChunks - i * kStageChunks;   // blocks from there on
+            if constexpr (WORDS) {
+                v[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)((off + 4 * i) | outside_if(room <= 0)), 0, 0);
+            } else {
+                uint32_t w = 0;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        w |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
-                                 rs, (int)((off + 4 * i + 2 * g + j) | outside_if(room <= 2 * g + j)), 0, 0)
-                             << (8 * j);
-                    v[i] = w << (16 * g);
-                }
+                for (int j = 0; j < 2; ++j)
+                    w |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
+                             rs, (int)((off + 4 * i + 2 * g + j) | outside_if(room <= 2 * g + j)), 0, 0)
+                         << (8 * j);
+                v[i] = w << (16 * g);
             }
         }
         return v;
     };
     u32x4 qw[NT], qa[MT], next_qw[NT], next_qa[MT];
-    auto load_group = [&](int group, auto whole) {
+    auto load_scales = [&](int group, auto load) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int tr = wn * NT + i;
-            next_qw[i] = scale16(SWIGLU && (i & 1) ? rsu : rsw, weight_row(tr * 32) + r, group, whole);
+            next_qw[i] = load(SWIGLU && (i & 1) ? rsu : rsw, weight_row(tr * 32) + r, group);
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i) next_qa[i] = scale16(rsa, (wm * MT + i) * 32 + r, group, whole);
+        for (int i = 0; i < MT; ++i) next_qa[i] = load(rsa, (wm * MT + i) * 32 + r, group);
     };
-    auto load_scales = [&](int group) {
-        if (WORDS && (group + 1) * kGroupChunks <= nblk) load_group(group, std::true_type{});
-        else load_group(group, std::false_type{});
+    // Both halves of a wave get the lower half's group (HALF 0) or the upper half's.
+    auto of_half = [](u32x4 v, auto half) {
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = __builtin_amdgcn_permlane32_swap(v[i], v[i], false, false)[decltype(half)::value];
+        return o;
     };
-    auto take_scales = [&] {
+    auto take_half = [&](auto half) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) qw[i] = of_half(next_qw[i], half);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) qa[i] = of_half(next_qa[i], half);
+    };
+    auto take_rest = [&] {
 #pragma unroll
         for (int i = 0; i < NT; ++i) qw[i] = next_qw[i];
 #pragma unroll
@@ -341,7 +342,15 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
     MOE_MX_STEP(1);                \
     ++s
 
-    load_scales(0);
+// The whole group that begins with stage s.
+#define MOE_MX_GROUP()              \
+    MOE_MX_STAGE(lds0, lds1, 0);    \
+    MOE_MX_STAGE(lds1, lds2, 1);    \
+    MOE_MX_STAGE(lds2, lds3, 2);    \
+    MOE_MX_STAGE(lds3, lds0, 3)
+
+    const int pairs = WORDS ? nblk / (2 * kGroupChunks) : 0;
+    if constexpr (WORDS) load_scales(0, scale_pair);
     load_stage(lds0, 0);
     load_stage(lds1, 1);      // past the last stage: zeros
     load_stage(lds2, 2);
@@ -351,15 +360,20 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
     int s = 0;
     sync(std::integral_constant<int, 3 * kLoads>{});
     read_frags(0, lds0);
+    for (int p = 1; p <= pairs; ++p) {
+        take_half(std::integral_constant<int, 0>{});
+        MOE_MX_GROUP();
+        take_half(std::integral_constant<int, 1>{});
+        load_scales(2 * p, scale_pair);     // behind the last pair: not used
+        MOE_MX_GROUP();
+    }
+    if (s < stages) load_scales(2 * pairs, scale_rest);
     while (s + kGroup <= stages) {
-        take_scales();
-        load_scales(s / kGroup + 1);
-        MOE_MX_STAGE(lds0, lds1, 0);
-        MOE_MX_STAGE(lds1, lds2, 1);
-        MOE_MX_STAGE(lds2, lds3, 2);
-        MOE_MX_STAGE(lds3, lds0, 3);
+        take_rest();
+        load_scales(s / kGroup + 1, scale_rest);
+        MOE_MX_GROUP();
     }
-    take_scales();
+    take_rest();
     if (s < stages) {
         MOE_MX_STAGE(lds0, lds1, 0);
     }
@@ -369,43 +383,58 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
     if (s < stages) {
         MOE_MX_STAGE(lds2, lds3, 2);
     }
+#undef MOE_MX_GROUP
 #undef MOE_MX_STAGE
 #undef MOE_MX_STEP
-    // no load into LDS may be in flight when the workgroup's LDS goes to the next one
-    __builtin_amdgcn_s_waitcnt(0);
+    // No load into LDS may be in flight when it is written below, or goes to the next
+    // workgroup.
+    sync(std::integral_constant<int, 0>{});
 
-    // a lane holds columns r of the tile (a row of y) and weight rows 8 * p + 4 * g + 0..3
+    // A lane holds column r of a tile (a row of y) and weight rows 8 * p + 4 * g + 0..3 of it:
+    // stores of its own values would be 8 bytes to a row.  Each wave turns 32 rows at a time
+    // in its quarter of the LDS and stores whole stretches of a row, 16 bytes a lane.
+    constexpr int kCols = NT * 32 / (SWIGLU ? 2 : 1);     // output columns of a wave
+    static_assert(32 * (kCols * 4 + 16) <= sizeof(lds0), "a wave's 32 rows fit one buffer");
+    uint8_t* turn = wave == 0 ? lds0 : wave == 1 ? lds1 : wave == 2 ? lds2 : lds3;
+    const int64_t c0 = n0 + wn * kCols;
+    auto store_rows = [&](auto f32) {
+        constexpr bool F32 = decltype(f32)::value;
+        constexpr int kEl = F32 ? 4 : 2;
+        constexpr int kPitch = kCols * kEl + 16;          // spreads rows over the banks
+        constexpr int kLanes = kCols * kEl / 16;          // lanes of a row
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-        const int row = (wm * MT + j) * 32 + r;
-        if (row >= t.rows) continue;
-        const int64_t out = (t.row0 + row) * NO;
-        if constexpr (SWIGLU) {
+        for (int j = 0; j < MT; ++j) {
+            const int row0 = (wm * MT + j) * 32;
+            if (row0 >= t.rows) break;
 #pragma unroll
-            for (int i = 0; i < NT; i += 2)
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const int64_t n = n0 + (wn * NT + i) / 2 * 32 + 8 * p + 4 * g;
-                    if (n >= NO) continue;
-                    f32x4 v;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        v[q] = silu_of(acc[i][j][4 * p + q]) * acc[i + 1][j][4 * p + q];
-                    store4(a.y, a.y_f32, out + n, v);
-                }
-        } else {
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT; i += SWIGLU ? 2 : 1)
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    const int64_t n = n0 + (wn * NT + i) * 32 + 8 * p + 4 * g;
-                    if (n >= NO) continue;
-                    const f32x4 v = {acc[i][j][4 * p], acc[i][j][4 * p + 1], acc[i][j][4 * p + 2],
-                                     acc[i][j][4 * p + 3]};
-                    store4(a.y, a.y_f32, out + n, v);
+                    float v[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float z = acc[i][j][4 * p + q];
+                        if constexpr (SWIGLU) v[q] = silu_of(z) * acc[i + 1][j][4 * p + q];
+                        else v[q] = z;
+                    }
+                    uint8_t* at = turn + r * kPitch + (i / (SWIGLU ? 2 : 1) * 32 + 8 * p + 4 * g) * kEl;
+                    if constexpr (F32) *(f32x4*)at = f32x4{v[0], v[1], v[2], v[3]};
+                    else *(u32x2*)at = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
                 }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int k = 0; k < 32 * kLanes / kWave; ++k) {
+                const int row = k * (kWave / kLanes) + lane / kLanes;
+                const int64_t n = c0 + lane % kLanes * (16 / kEl);
+                const u32x4 v = *(const u32x4*)(turn + row * kPitch + lane % kLanes * 16);
+                if (row0 + row < t.rows && n < NO)
+                    st16((uint8_t*)a.y + ((t.row0 + row0 + row) * NO + n) * kEl, v);
+            }
+            __builtin_amdgcn_wave_barrier();
         }
-    }
+    };
+    if (a.y_f32) store_rows(std::true_type{});
+    else store_rows(std::false_type{});
 }
 
 template <int BM, int WM>

@@ -150,26 +150,21 @@ __device__ __forceinline__ float silu_of(float g) {
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
 }
 
-// WM x WN waves: a wave owns BM / WM rows and kBN / WN weight rows.
-// WORDS: every row's scales start and end at a whole word.
-template <int BM, int WM, bool SWIGLU, bool WORDS>
-__global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int col_tiles,
-                                                              int64_t base) {
-    constexpr int WN = kWaves / WM;
+// Waves that share a tile's weight rows.
+constexpr int row_waves(int BM) { return BM >= 128 ? 2 : 1; }
+
+// One tile of at most BM rows by kBN weight rows: WM x WN waves, each BM / WM rows and kBN /
+// WN weight rows.  WORDS: every row's scales start and end at a whole word.
+template <int BM, bool SWIGLU, bool WORDS, int LDS>
+__device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t, int col,
+                                             uint8_t (&lds0)[LDS], uint8_t (&lds1)[LDS],
+                                             uint8_t (&lds2)[LDS], uint8_t (&lds3)[LDS]) {
+    constexpr int WM = row_waves(BM), WN = kWaves / WM;
     constexpr int MT = BM / WM / 32, NT = kBN / WN / 32;
     constexpr int kLoadsA = (BM / 16 + kWaves - 1) / kWaves, kLoadsW = kBN / 16 / kWaves;
     constexpr int kA = BM * kStageBytes;     // where a stage's weight rows begin
-    __shared__ __align__(16) uint8_t lds0[kA + kBN * kStageBytes], lds1[kA + kBN * kStageBytes];
-    __shared__ __align__(16) uint8_t lds2[kA + kBN * kStageBytes], lds3[kA + kBN * kStageBytes];
+    static_assert(kA + kBN * kStageBytes <= LDS, "a stage fits its buffer");
 
-    int col = 0;
-    Tile t = find_tile<BM>(a, base + blockIdx.x, col_tiles, col);
-    // the same in every lane: into scalar registers, where descriptors have to be
-    t.e = __builtin_amdgcn_readfirstlane(t.e);
-    t.row0 = uniform(t.row0);
-    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
-    col = __builtin_amdgcn_readfirstlane(col);
-    if (t.e < 0) return;
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave / WN, wn = wave % WN;
@@ -394,7 +389,7 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
     // stores of its own values would be 8 bytes to a row.  Each wave turns 32 rows at a time
     // in its quarter of the LDS and stores whole stretches of a row, 16 bytes a lane.
     constexpr int kCols = NT * 32 / (SWIGLU ? 2 : 1);     // output columns of a wave
-    static_assert(32 * (kCols * 4 + 16) <= sizeof(lds0), "a wave's 32 rows fit one buffer");
+    static_assert(32 * (kCols * 4 + 16) <= LDS, "a wave's 32 rows fit one buffer");
     uint8_t* turn = wave == 0 ? lds0 : wave == 1 ? lds1 : wave == 2 ? lds2 : lds3;
     const int64_t c0 = n0 + wn * kCols;
     auto store_rows = [&](auto f32) {
@@ -437,7 +432,30 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
     else store_rows(std::false_type{});
 }
 
-template <int BM, int WM>
+// A tile of up to 128 rows that is half full at the most is worked on as one of half the
+// height: 4096 rows of 64 experts (4096 x 7168) 241 -> 232 us, 8192 295 -> 285.  (At 256 rows
+// it did not pay: 650 -> 659 us for 32768 rows.)
+template <int BM, bool SWIGLU, bool WORDS>
+__global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int col_tiles,
+                                                              int64_t base) {
+    constexpr int kLds = (BM + kBN) * kStageBytes;
+    __shared__ __align__(16) uint8_t lds0[kLds], lds1[kLds], lds2[kLds], lds3[kLds];
+    int col = 0;
+    Tile t = find_tile<BM>(a, base + blockIdx.x, col_tiles, col);
+    // the same in every lane: into scalar registers, where descriptors have to be
+    t.e = __builtin_amdgcn_readfirstlane(t.e);
+    t.row0 = uniform(t.row0);
+    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    col = __builtin_amdgcn_readfirstlane(col);
+    if (t.e < 0) return;
+    constexpr bool kHalves = BM <= 128;
+    if (kHalves && t.rows <= BM / 2)
+        product_tile<(kHalves ? BM / 2 : BM), SWIGLU, WORDS>(a, t, col, lds0, lds1, lds2, lds3);
+    else
+        product_tile<BM, SWIGLU, WORDS>(a, t, col, lds0, lds1, lds2, lds3);
+}
+
+template <int BM>
 hipError_t launch(const ProductArgs& a, hipStream_t s) {
     const int64_t cols = a.swiglu ? a.N / 2 : a.N;
     const int col_tiles = (int)((cols + (a.swiglu ? kBN / 2 : kBN) - 1) / (a.swiglu ? kBN / 2 : kBN));
@@ -448,11 +466,11 @@ hipError_t launch(const ProductArgs& a, hipStream_t s) {
     for (int64_t base = 0; base < blocks; base += kMaxGrid) {
         const dim3 grid((unsigned)(blocks - base < kMaxGrid ? blocks - base : kMaxGrid));
         if (a.swiglu) {
-            if (words) product_kernel<BM, WM, true, true><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
-            else product_kernel<BM, WM, true, false><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
+            if (words) product_kernel<BM, true, true><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
+            else product_kernel<BM, true, false><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
         } else {
-            if (words) product_kernel<BM, WM, false, true><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
-            else product_kernel<BM, WM, false, false><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
+            if (words) product_kernel<BM, false, true><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
+            else product_kernel<BM, false, false><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
         }
     }
     return hipGetLastError();
@@ -462,11 +480,13 @@ hipError_t launch(const ProductArgs& a, hipStream_t s) {
 
 hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
+    // Tile heights 64, 128, 256 by the mean rows of an expert, in us (32 experts with uneven
+    // loads, 4096 x 4096): mean 24 62, 64, 72; 64 73, 75, 82; 96 91, 90, 94; 192 135, 117, 122;
+    // 256 163, 148, 128; 384 224, 200, 185.
     const int64_t mean = a.rows / a.E;
-    if (mean <= 32) return launch<32, 1>(a, s);
-    if (mean <= 64) return launch<64, 1>(a, s);
-    if (mean <= 128) return launch<128, 2>(a, s);
-    return launch<256, 2>(a, s);
+    if (mean <= 64) return launch<64>(a, s);
+    if (mean < 224) return launch<128>(a, s);
+    return launch<256>(a, s);
 }
 
 }  // namespace moe

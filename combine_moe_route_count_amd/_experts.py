@@ -42,7 +42,7 @@ def _lib() -> ctypes.CDLL:
             fn = getattr(lib, name)
             fn.argtypes = args
             fn.restype = ctypes.c_int
-        lib.moe_experts_decode_workspace_size.argtypes = [_I64, _I32, _I64]
+        lib.moe_experts_decode_workspace_size.argtypes = [_I64, _I32, _I64, _I64]
         lib.moe_experts_decode_workspace_size.restype = _SZ
         _bound = lib
     return _bound
@@ -126,14 +126,15 @@ def expert_product_mxfp4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tenso
     return y
 
 
-def experts_decode_workspace_size(T: int, K: int, I: int) -> int:
-    return int(_lib().moe_experts_decode_workspace_size(T, K, I))
+def experts_decode_workspace_size(T: int, K: int, I: int, H: int = 8192) -> int:
+    return int(_lib().moe_experts_decode_workspace_size(T, K, H, I))
 
 
-def experts_decode_workspace(T: int, K: int, I: int, device="cuda") -> torch.Tensor:
-    """A device workspace of experts_decode for these sizes, and for any smaller ones
-    (256-byte aligned, needs no initialisation)."""
-    n = max(experts_decode_workspace_size(T, K, I), 1)
+def experts_decode_workspace(T: int, K: int, I: int, H: int = 8192, device="cuda") -> torch.Tensor:
+    """A device workspace of experts_decode for these sizes, and for any smaller ones: a
+    program keeps one for its largest batch and layer (256-byte aligned, needs no
+    initialisation).  The default H covers token rows of up to 8192 elements."""
+    n = max(experts_decode_workspace_size(T, K, I, H), 1)
     buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
     off = (-buf.data_ptr()) % 256
     return buf[off:off + n]
@@ -168,7 +169,7 @@ def experts_decode(x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, w13: tor
         out = torch.empty((T, H), dtype=out_dtype, device=dev)
     _tensor("out", out, (T, H), _FLOAT, dev)
     if ws is None:
-        ws = experts_decode_workspace(T, K, I, torch.device("cuda", dev))
+        ws = experts_decode_workspace(T, K, I, H, torch.device("cuda", dev))
     else:
         _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.is_cuda and ws.get_device() == dev,
               f"ws must be contiguous uint8 on cuda:{dev}")

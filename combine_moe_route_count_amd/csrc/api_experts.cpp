@@ -135,11 +135,12 @@ MOE_API int moe_expert_product_mxfp4(const void* a, const void* a_scales, int64_
     return MOE_OK;
 }
 
-MOE_API size_t moe_experts_decode_workspace_size(int64_t T, int K, int64_t I) {
-    if (T < 0 || K < 1 || K > 16 || T > moe::kDecodeEntries || T * K > moe::kDecodeEntries || I <= 0 ||
-        I % 8 != 0 || I > ((int64_t)1 << 24))
+MOE_API size_t moe_experts_decode_workspace_size(int64_t T, int K, int64_t H, int64_t I) {
+    if (T < 0 || K < 1 || K > 16 || T > moe::kDecodeEntries || T * K > moe::kDecodeEntries)
         return 0;
-    return moe::decode_ws(T, K, I);
+    for (int64_t n : {H, I})
+        if (n <= 0 || n % 8 != 0 || n > moe::kDecodeLength) return 0;
+    return moe::decode_ws(T, K, H, I);
 }
 
 MOE_API int moe_experts_decode(const void* x, int64_t T, int64_t H, const int32_t* idx,
@@ -153,6 +154,8 @@ MOE_API int moe_experts_decode(const void* x, int64_t T, int64_t H, const int32_
         return fail(MOE_ERR_INVALID_ARG, "weight dtype must be MOE_BF16 or MOE_FP4_E2M1");
     MOE_TRY(check_len(H, mx ? moe::kMxBlock : 8, "H"));
     MOE_TRY(check_len(I, mx ? moe::kMxBlock : 8, "I"));
+    if (H > moe::kDecodeLength || I > moe::kDecodeLength)
+        return fail(MOE_ERR_INVALID_ARG, "H=%lld or I=%lld exceeds 2^20", (long long)H, (long long)I);
     if (K < 1 || K > 16) return fail(MOE_ERR_INVALID_ARG, "K=%d must be in [1,16]", K);
     if (T < 0 || T > moe::kDecodeEntries || T * K > moe::kDecodeEntries)
         return fail(MOE_ERR_INVALID_ARG, "T=%lld with K=%d: T*K must be in [0, %d]", (long long)T, K,
@@ -166,7 +169,7 @@ MOE_API int moe_experts_decode(const void* x, int64_t T, int64_t H, const int32_
     if (mx != (w13_scales != nullptr) || mx != (w2_scales != nullptr))
         return fail(MOE_ERR_INVALID_ARG, "w13_scales and w2_scales go with MOE_FP4_E2M1 weights alone");
     MOE_TRY(check_rows_ptr(out, T, "out"));
-    const size_t need = moe::decode_ws(T, K, I);
+    const size_t need = moe::decode_ws(T, K, H, I);
     MOE_TRY(moe::check_ws(ws, ws_bytes, need));
     const int64_t wb = (int64_t)E * H * I * (mx ? 1 : 4) / 2, sb = (int64_t)E * H * I / moe::kMxBlock;
     MOE_TRY(check_all_apart({{out, T * H * float_bytes(out_dt), "out"}, {ws, (int64_t)need, "ws"}},

@@ -65,7 +65,8 @@ struct ProductArgs {
 hipError_t launch_product(const ProductArgs& a, hipStream_t s);
 
 // The whole experts' step of a few tokens.
-constexpr int kDecodeEntries = 1024;   // most T*K
+constexpr int kDecodeEntries = 1024;              // most T*K
+constexpr int64_t kDecodeLength = (int64_t)1 << 20;   // most H and I
 struct DecodeArgs {
     const uint16_t* x;          // [T,H] bf16
     int64_t T, H, I;
@@ -80,7 +81,7 @@ struct DecodeArgs {
     bool out_f32;
     void* ws;
 };
-size_t decode_ws(int64_t T, int K, int64_t I);
+size_t decode_ws(int64_t T, int K, int64_t H, int64_t I);
 hipError_t launch_experts_decode(const DecodeArgs& a, hipStream_t s);
 
 }  // namespace moe

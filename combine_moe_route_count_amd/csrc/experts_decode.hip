@@ -1,21 +1,23 @@
-// experts_decode.hip - the whole experts' step of a few tokens, in two kernels:
+// experts_decode.hip - the whole experts' step of a few tokens:
 //   h[f]   = silu(W1[e] x[t]) * (W3[e] x[t])        for every entry f = t*K + k, e = idx[f]
-//   out[t] = sum over k of w[t,k] * W2[e] h[t*K + k]
+//   y[f]   = W2[e] h[f]
+//   out[t] = sum over k of w[t,k] * y[t*K + k]
 // There is nothing to do here but to read the weights of the experts in use once; their
-// bytes over the HBM rate are the floor.  So no token row is packed or moved: each
-// kernel walks the experts in use, streams their weights from HBM straight into matrix
-// fragments, 16 weight rows by 16 entries, and looks its entries up.
+// bytes over the HBM rate are the floor.  So no token row is packed or moved: the two
+// products walk the experts in use, 32 weight rows of a wave by 16 entries (or 32) at a
+// time, and look their entries up; a short third kernel adds a token's results.
 //
-// Weights are the rows of v_mfma 16x16x32 bf16: lane l holds row l % 16 and 8
-// consecutive k.  MXFP4 weights are widened to bf16 in registers (e2m1 times a power of
-// two is exact in bf16): lane group g = l / 16 takes block g of 4 and uses its 32 codes
-// in 4 matrix steps, so its codes are one 16-byte load and its scale one byte.
+// Weights are the rows of v_mfma 16x16x32 bf16: lane l holds row l % 16 and 8 consecutive
+// k.  MXFP4 weights are widened to bf16 in registers (e2m1 times a power of two is exact
+// in bf16): lane group g = l / 16 takes block g of 4 and uses its 32 codes in 4 matrix
+// steps.
 //
-// Up kernel: a workgroup takes (expert, 16 rows of W1 and of W3), its 4 waves a quarter of
-// H each; the partial sums are joined in LDS in order of the waves, and h goes to the
-// workspace.  Down kernel: a workgroup owns 16 outputs and walks all experts in use, one
-// wave an expert (or a part of I where experts are few); every entry's result is kept in
-// LDS and a token's are added in ascending k, as moe_combine adds them.
+// K runs in stages of 64 elements (MXFP4: 128): weight rows and the entries' rows go
+// straight into LDS, four stages deep, so that three are in flight while one is used.  What
+// runs dry costs most here, so the stages of a workgroup's items (expert, weight rows)
+// form one stream: the last stages of an item are used while the first of the next one
+// are on their way.  Items have the same number of stages, filled up to a multiple of four
+// with stages of zeros, so that every LDS buffer is a fixed one in the code.
 //
 // h between the products is held in as many bf16 parts as the result can show: 2 (16 bits
 // of significand) for a bf16 result, 3 (24 bits) for an f32 one.  Each part costs one
@@ -24,6 +26,7 @@
 
 #include "train_device.hpp"
 #include "experts.hpp"
+#include "internal.hpp"
 
 namespace moe {
 
@@ -32,47 +35,48 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kUpThreads = 256, kUpWaves = kUpThreads / kWave;
-constexpr int kDownThreads = 512, kDownWaves = kDownThreads / kWave;
-constexpr int kMaxEntries = kDecodeEntries;
+using Lds = __attribute__((address_space(3))) uint8_t;
 
-// The experts in use and their entries: expert ids[a] has entries ent[start[a]] ..
-// ent[start[a+1]-1], in ascending order.
+constexpr int kMaxEntries = kDecodeEntries;
+constexpr int kGroup = 4;      // stages in LDS
+
+// The work of one pass over an expert's weights: up to `width` of its entries.  Slot s
+// belongs to expert[s] and has the entries ent[first[s]] .. ent[first[s + 1] - 1].
 struct Lists {
     int n;
-    uint16_t ids[kMaxEntries];
-    uint16_t start[kMaxEntries + 1];
+    uint16_t expert[kMaxEntries];
+    uint16_t first[kMaxEntries + 2];
     uint16_t ent[kMaxEntries];
 };
+static_assert(sizeof(Lists) % 4 == 0, "copied by words");
+constexpr size_t kListBytes = (sizeof(Lists) + 255) / 256 * 256;
 
 // Builds the lists from the ids, by the whole workgroup.  cnt and sum are scratch.
 template <int THREADS>
-__device__ void build_lists(const int32_t* idx, int N, int E, Lists& l, int (&cnt)[1024],
-                            int (&sum)[THREADS / kWave][2]) {
+__device__ void build_lists(const int32_t* idx, int N, int E, int width, Lists& l,
+                            int (&cnt)[1024], int (&sum)[THREADS / kWave][2]) {
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     for (int e = tid; e < E; e += THREADS) cnt[e] = 0;
     __syncthreads();
     constexpr int kPer = kMaxEntries / THREADS;
-    int mine[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int f = tid * kPer + i;
+        const int f = tid + i * THREADS;
         const int e = f < N ? idx[f] : -1;
-        mine[i] = e >= 0 && e < E ? e : -1;
-        if (mine[i] >= 0) atomicAdd(&cnt[mine[i]], 1);
+        if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
     }
     __syncthreads();
-    // exclusive sums over the experts, of "in use" and of entries
+    // exclusive sums over the experts, of slots and of entries
     constexpr int kPerE = 1024 / THREADS;
-    int used = 0, total = 0;
+    int slots = 0, total = 0;
 #pragma unroll
     for (int i = 0; i < kPerE; ++i) {
         const int e = tid * kPerE + i;
         const int c = e < E ? cnt[e] : 0;
-        used += c > 0;
+        slots += (c + width - 1) / width;
         total += c;
     }
-    int u = used, t = total;
+    int u = slots, t = total;
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) {
         const int ou = __shfl_up(u, d), ot = __shfl_up(t, d);
@@ -86,7 +90,7 @@ __device__ void build_lists(const int32_t* idx, int N, int E, Lists& l, int (&cn
         sum[wave][1] = t;
     }
     __syncthreads();
-    int a = u - used, at = t - total, all = 0, all_ent = 0;
+    int a = u - slots, at = t - total, all = 0, entries = 0;
 #pragma unroll
     for (int i = 0; i < THREADS / kWave; ++i) {
         if (i < wave) {
@@ -94,15 +98,15 @@ __device__ void build_lists(const int32_t* idx, int N, int E, Lists& l, int (&cn
             at += sum[i][1];
         }
         all += sum[i][0];
-        all_ent += sum[i][1];
+        entries += sum[i][1];
     }
 #pragma unroll
     for (int i = 0; i < kPerE; ++i) {
         const int e = tid * kPerE + i;
         const int c = e < E ? cnt[e] : 0;
-        if (c > 0) {
-            l.ids[a] = (uint16_t)e;
-            l.start[a] = (uint16_t)at;
+        for (int j = 0; j < c; j += width) {
+            l.expert[a] = (uint16_t)e;
+            l.first[a] = (uint16_t)(at + j);
             ++a;
         }
         if (e < E) cnt[e] = at;    // from here on: where the expert's next entry goes
@@ -110,60 +114,30 @@ __device__ void build_lists(const int32_t* idx, int N, int E, Lists& l, int (&cn
     }
     if (tid == 0) {
         l.n = all;
-        l.start[all] = (uint16_t)all_ent;
+        l.first[all] = (uint16_t)entries;
     }
     __syncthreads();
-    // an entry's place among its expert's does not change any result: a column of a
-    // matrix fragment does not depend on its neighbours
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        if (mine[i] >= 0) l.ent[atomicAdd(&cnt[mine[i]], 1)] = (uint16_t)(tid * kPer + i);
-    __syncthreads();
-}
-
-// ---------------------------------------------------------------------------
-// acc[r][c] += A[16 rows of tile r][k0 .. k1) * B[k0 .. k1)[16 entries of tile c], B the sum
-// of P parts.  a[r]: the lane's weight row; b[c]: the lane's entry row, part p at + p*part.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
-
-__device__ __forceinline__ u32x4 zero4() { return u32x4{0, 0, 0, 0}; }
-
-template <int RT, int NT, int P>
-__device__ __forceinline__ void stream_bf16(f32x4 (&acc)[RT][NT], const uint16_t* (&a)[RT],
-                                            const uint16_t* (&b)[NT], int64_t part, int k0, int k1) {
-    constexpr int U = 8 / (RT < 2 ? 1 : RT);   // steps whose loads are in flight together
-    const int g8 = (threadIdx.x % kWave) / 16 * 8;
-    int k = k0;
-    auto step = [&](auto n, auto guarded) {
-        constexpr int STEPS = decltype(n)::value;
-        constexpr bool GUARD = decltype(guarded)::value;
-        u32x4 wa[STEPS][RT];
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const int at = k + s * 32 + g8;
-                wa[s][r] = !GUARD || at < k1 ? ld16_stream(a[r] + at) : zero4();
+    // Entries to their places, 64 at a time, in ascending order: every workgroup has to find
+    // the same lists.
+    const int bits = E > 1 ? 32 - __builtin_clz(E - 1) : 1;
+    for (int c = 0; c * kWave < N; ++c) {
+        if (c % (THREADS / kWave) == wave) {
+            const int f = c * kWave + lane;
+            int e = f < N ? idx[f] : -1;
+            if (e >= E || e < 0) e = -1;
+            const uint64_t same = match_key(e, bits);
+            const int base = e >= 0 ? cnt[e] : 0, rank = lanes_below(same);
+            __builtin_amdgcn_wave_barrier();
+            if (e >= 0) {
+                l.ent[base + rank] = (uint16_t)f;
+                if (rank == 0) cnt[e] = base + __popcll(same);
             }
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-#pragma unroll
-                for (int c = 0; c < NT; ++c) {
-                    const int at = k + s * 32 + g8;
-                    const u32x4 v = !GUARD || at < k1 ? ld16(b[c] + p * part + at) : zero4();
-#pragma unroll
-                    for (int r = 0; r < RT; ++r)
-                        acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(wa[s][r]), as_bf16(v),
-                                                                            acc[r][c], 0, 0, 0);
-                }
-        k += STEPS * 32;
-    };
-    while (k + U * 32 <= k1) step(std::integral_constant<int, U>{}, std::false_type{});
-    while (k < k1) step(std::integral_constant<int, 1>{}, std::true_type{});
+        }
+        __syncthreads();
+    }
 }
+
+__device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 // Two e2m1 codes (byte SEL of d) times 2^(scale's exponent), as bf16.
 template <int SEL>
@@ -177,278 +151,401 @@ __device__ __forceinline__ u32x4 widen8(uint32_t d, float scale) {
     return u32x4{widen2<0>(d, scale), widen2<1>(d, scale), widen2<2>(d, scale), widen2<3>(d, scale)};
 }
 
-// a[r]: codes of the lane's weight row; sc[r]: its scales.
-template <int RT, int NT, int P>
-__device__ __forceinline__ void stream_mxfp4(f32x4 (&acc)[RT][NT], const uint8_t* (&a)[RT],
-                                             const uint8_t* (&sc)[RT], const uint16_t* (&b)[NT],
-                                             int64_t part, int k0, int k1) {
-    constexpr int U = 4 / (RT < 2 ? 1 : RT);
-    const int g = (threadIdx.x % kWave) / 16;
-    int k = k0;
-    auto step = [&](auto n, auto guarded) {
-        constexpr int STEPS = decltype(n)::value;
-        constexpr bool GUARD = decltype(guarded)::value;
-        u32x4 codes[STEPS][RT];
-        uint32_t scale[STEPS][RT];
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const int blk = (k >> 5) + s * 4 + g;
-                const bool in = !GUARD || blk * 32 < k1;
-                codes[s][r] = in ? ld16_stream(a[r] + blk * 16) : zero4();
-                scale[s][r] = in ? sc[r][blk] : 0u;
-            }
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int at = k + s * 128 + g * 32;
-            const bool in = !GUARD || at < k1;
-            float f[RT];
-            bool nan[RT];
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const uint32_t e = scale[s][r];
-                nan[r] = e == 255u;
-                f[r] = __builtin_bit_cast(float, e << 23);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                u32x4 wa[RT];
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    wa[r] = widen8(codes[s][r][q], f[r]);
-                    if (nan[r]) wa[r] = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
-                }
-#pragma unroll
-                for (int p = 0; p < P; ++p)
-#pragma unroll
-                    for (int c = 0; c < NT; ++c) {
-                        const u32x4 v = in ? ld16(b[c] + p * part + at + q * 8) : zero4();
-#pragma unroll
-                        for (int r = 0; r < RT; ++r)
-                            acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                as_bf16(wa[r]), as_bf16(v), acc[r][c], 0, 0, 0);
-                    }
-            }
-        }
-        k += STEPS * 128;
-    };
-    while (k + U * 128 <= k1) step(std::integral_constant<int, U>{}, std::false_type{});
-    while (k < k1) step(std::integral_constant<int, 1>{}, std::true_type{});
-}
-
-// The lane's rows of RT tiles of 16 weight rows of [.., K], and their products with the
-// entries' rows, over [k0, k1).
-template <bool MX, int RT, int NT, int P>
-__device__ __forceinline__ void stream(f32x4 (&acc)[RT][NT], const void* w, const uint8_t* scales,
-                                       const int64_t (&row)[RT], int64_t K, const uint16_t* (&b)[NT],
-                                       int64_t part, int k0, int k1) {
-    if constexpr (MX) {
-        const uint8_t *a[RT], *sc[RT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            a[r] = (const uint8_t*)w + row[r] * (K / 2);
-            sc[r] = scales + row[r] * (K / 32);
-        }
-        stream_mxfp4<RT, NT, P>(acc, a, sc, b, part, k0, k1);
-    } else {
-        const uint16_t* a[RT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) a[r] = (const uint16_t*)w + row[r] * K;
-        stream_bf16<RT, NT, P>(acc, a, b, part, k0, k1);
-    }
-}
-
-// Part `part` of `parts` of [0, K), in whole steps.
-template <bool MX>
-__device__ __forceinline__ void k_range(int64_t K, int part, int parts, int& k0, int& k1) {
-    constexpr int kStep = MX ? 128 : 32;
-    const int steps = (int)((K + kStep - 1) / kStep);
-    const int per = (steps + parts - 1) / parts;
-    const int64_t lo = (int64_t)part * per * kStep, hi = lo + (int64_t)per * kStep;
-    k0 = (int)(lo < K ? lo : K);
-    k1 = (int)(hi < K ? hi : K);
-}
-
 __device__ __forceinline__ float silu_of(float g) {
     // g / (1 + exp(-g)); exp overflows to an infinity below -88, where the quotient is -0
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
 }
 
-// v as a sum of P bf16 values, each the rounding of what the ones before it left.
-template <int P>
-__device__ __forceinline__ void split_store(uint16_t* h, int64_t part, float v) {
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const __bf16 b = (__bf16)v;
-        h[p * part] = __builtin_bit_cast(uint16_t, b);
-        // an infinity or a NaN stands in the first part alone
-        v = p == 0 && !__builtin_isfinite(v) ? 0.0f : v - (float)b;
-    }
+// Ored to an offset below 2^31 it leaves every descriptor's range (2^31 at the most).
+__device__ __forceinline__ uint32_t outside_if(bool b) { return (uint32_t)b << 31; }
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* base, int64_t row,
+                                                          int64_t rows, int64_t row_bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((char*)base + row * row_bytes, 0,
+                                             (int)(uint32_t)(rows * row_bytes), kRsrcWord3);
 }
 
-constexpr int kCols = 4;     // column tiles of 16 entries that are worked on together
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (Lds*)lds, 16, (int)off, 0, 0, 0);
+}
 
-template <bool MX, int P>
-__global__ __launch_bounds__(kUpThreads) void up_kernel(DecodeArgs a, Lists* out_lists, uint16_t* h) {
+// One of the two products.  UP: the rows are those of W1 and W3, a wave has 16 of each, the
+// other factor is x (one part); else they are those of W2, 32 of a wave, times the P
+// parts of h.  NT: 16 entries per wave and pass times NT.
+template <bool MX, bool UP, int P, int NT, int WAVES>
+struct Stream {
+    static constexpr int kThreads = WAVES * kWave;
+    static constexpr int kStageK = MX ? 128 : 64;
+    static constexpr int kRowBytes = MX ? 64 : 128;             // of a weight row in a stage
+    static constexpr int kRowChunks = kRowBytes / 16;
+    static constexpr int kRowsPer = kWave / kRowChunks;         // weight rows per load
+    static constexpr int kLoadsW = 32 / kRowsPer;
+    static constexpr int kColChunks = kStageK / 8;              // 16-byte chunks of an entry's row
+    static constexpr int kColsPer = kWave / kColChunks;
+    static constexpr int kColLoads = 16 * NT / kColsPer;        // loads of one part of all entries
+    static constexpr int kLoadsB = (kColLoads + WAVES - 1) / WAVES;   // of a wave and part
+    static constexpr int kPart = 16 * NT * kColChunks * 16;
+    static constexpr int kW = WAVES * 32 * kRowBytes;
+    static constexpr int kStageBytes = kW + P * kPart;
+    static constexpr int kRows = WAVES * (UP ? 16 : 32);        // output rows of an item
+    static constexpr int kLoads = kLoadsW + P * kLoadsB;        // of a wave for a stage
+};
+
+// Where the stream is: the first weight row of an item and how many there are, and the
+// offsets of the entries' rows that the calling lane loads.
+template <int LB>
+struct Cursor {
+    int64_t row;
+    int rows;
+    uint32_t col[LB];
+};
+
+template <bool MX, bool UP, int P, int NT, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, Lists* lists,
+                                                               uint16_t* h, int64_t h_part,
+                                                               float* y, int h_parts, int words) {
+    using S = Stream<MX, UP, P, NT, WAVES>;
+    constexpr int kThreads = S::kThreads;
     __shared__ Lists l;
-    __shared__ int cnt[1024];
-    __shared__ int sum[kUpWaves][2];
-    __shared__ float red[kUpWaves][2][16][kCols * 16];
+    __shared__ __align__(16) uint8_t lds0[S::kStageBytes], lds1[S::kStageBytes];
+    __shared__ __align__(16) uint8_t lds2[S::kStageBytes], lds3[S::kStageBytes];
     const int N = (int)(a.T * a.K);
-    build_lists<kUpThreads>(a.idx, N, a.E, l, cnt, sum);
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < (int)(sizeof(Lists) / 4); i += kUpThreads)
-            ((uint32_t*)out_lists)[i] = ((const uint32_t*)&l)[i];
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int64_t part = (int64_t)N * a.I;
-    const int slices = (int)((a.I + 15) / 16);
-    int k0, k1;
-    k_range<MX>(a.H, wave, kUpWaves, k0, k1);
-    for (int item = blockIdx.x; item < l.n * slices; item += gridDim.x) {
-        const int who = item / slices, i0 = (item - who * slices) * 16;
-        const int e = l.ids[who], first = l.start[who], n = l.start[who + 1] - first;
-        int64_t i = i0 + lane % 16;
-        if (i >= a.I) i = a.I - 1;            // rows that are not there: computed, not stored
-        const int64_t row[2] = {(int64_t)e * 2 * a.I + i, (int64_t)e * 2 * a.I + a.I + i};
-        auto columns = [&](auto nt, int c0) {
-            constexpr int NT = decltype(nt)::value;
-            const uint16_t* b[NT];
+    if constexpr (UP) {
+        // the scratch of the lists is in the stages' space, which is not in use yet
+        static_assert(sizeof(int[1024]) <= S::kStageBytes, "scratch");
+        int(&cnt)[1024] = *reinterpret_cast<int(*)[1024]>(lds0);
+        int(&sum)[WAVES][2] = *reinterpret_cast<int(*)[WAVES][2]>(lds1);
+        build_lists<kThreads>(a.idx, N, a.E, 16 * NT, l, cnt, sum);
+        if (blockIdx.x == 0)
+            for (int i = threadIdx.x; i < (int)(sizeof(Lists) / 4); i += kThreads)
+                ((uint32_t*)lists)[i] = ((const uint32_t*)&l)[i];
+    } else {
+        for (int i = threadIdx.x; i < (int)(sizeof(Lists) / 4); i += kThreads)
+            ((uint32_t*)&l)[i] = ((const uint32_t*)lists)[i];
+        __syncthreads();
+    }
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t K = UP ? a.H : a.I, M = UP ? a.I : a.H;     // sum length, output rows of an expert
+    const int blocks = (int)((M + S::kRows - 1) / S::kRows);
+    const int items = __builtin_amdgcn_readfirstlane(l.n) * blocks;
+    const int chunks = (int)(MX ? K / 32 : K / 8), col_chunks = (int)(K / 8);
+    const int groups = (int)((K + S::kStageK * kGroup - 1) / (S::kStageK * kGroup));
+    const int64_t rb = MX ? K / 2 : K * 2, wrows = UP ? 2 * M : M;
+
+    auto item_rows = [&](int item, int& slot) {
+        slot = item / blocks;
+        return (int64_t)(item - slot * blocks) * S::kRows;
+    };
+    auto seek = [&](int item, Cursor<S::kLoadsB>& c) {
+        int slot;
+        const int64_t r0 = item_rows(item, slot);
+        const int e = __builtin_amdgcn_readfirstlane(l.expert[slot]);
+        const int first = __builtin_amdgcn_readfirstlane(l.first[slot]);
+        const int n = __builtin_amdgcn_readfirstlane(l.first[slot + 1]) - first;
+        c.row = (int64_t)e * wrows + r0;
+        c.rows = (int)(M - r0 < S::kRows ? M - r0 : S::kRows);
 #pragma unroll
-            for (int c = 0; c < NT; ++c) {
-                int col = c0 + c * 16 + lane % 16;
-                if (col >= n) col = n - 1;    // columns that are not there, likewise
-                b[c] = a.x + (int64_t)(l.ent[first + col] / a.K) * a.H;
+        for (int i = 0; i < S::kLoadsB; ++i) {
+            const int col = (wave * S::kLoadsB + i) % S::kColLoads * S::kColsPer + lane / S::kColChunks;
+            const int f = l.ent[first + (col < n ? col : 0)];
+            c.col[i] = (uint32_t)((UP ? f / a.K : f) * K * 2) | outside_if(col >= n);
+        }
+    };
+    // Stage s of an item into LDS.  A row's chunks stand at chunk ^ row bits, so that 8 lanes
+    // that read one chunk of 8 rows meet different banks.
+    const void* weights = UP ? a.w13 : a.w2;
+    auto load_stage = [&](uint8_t* lds, const Cursor<S::kLoadsB>& c, int s) {
+        const auto first = rows_of(weights, c.row, c.rows, rb);
+        const auto second = UP ? rows_of(weights, c.row + M, c.rows, rb) : first;
+#pragma unroll
+        for (int i = 0; i < S::kLoadsW; ++i) {
+            const int r = i * S::kRowsPer + lane / S::kRowChunks;     // of the wave's 32
+            const int at = s * S::kRowChunks + ((lane % S::kRowChunks) ^ (MX ? r / 2 % 4 : r % 8));
+            const int row = UP ? wave * 16 + r % 16 : wave * 32 + r;
+            to_lds(UP && i * S::kRowsPer >= 16 ? second : first, lds + (wave * 32 + i * S::kRowsPer) * S::kRowBytes,
+                   ((uint32_t)row * (uint32_t)rb + (uint32_t)at * 16) | outside_if(at >= chunks));
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const auto src = UP ? rows_of(a.x, 0, a.T, K * 2) : rows_of(h + p * h_part, 0, N, K * 2);
+#pragma unroll
+            for (int i = 0; i < S::kLoadsB; ++i) {
+                const int load = (wave * S::kLoadsB + i) % S::kColLoads;
+                const int col = load * S::kColsPer + lane / S::kColChunks;
+                const int at = s * S::kColChunks + ((lane % S::kColChunks) ^ (col % 8));
+                to_lds(src, lds + S::kW + p * S::kPart + load * 1024,
+                       (c.col[i] + (uint32_t)at * 16) | outside_if(at >= col_chunks));
             }
-            f32x4 acc[2][NT] = {};
-            stream<MX, 2, NT, 1>(acc, a.w13, a.s13, row, a.H, b, 0, k0, k1);
+        }
+    };
+    // The scales of a group of four stages: byte g of word i is that of the lane's block.
+    const int r = lane % 16, g = lane / 16;
+    const int nblk = (int)(K / 32);
+    u32x4 next_scale[2] = {};
+    auto load_scales = [&](const Cursor<S::kLoadsB>& c, int group) {
+        if constexpr (MX) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int i = 0; i < 2; ++i) {
+                const auto src = rows_of(UP ? a.s13 : a.s2, UP && i ? c.row + M : c.row, c.rows, nblk);
+                const uint32_t off = (uint32_t)(UP ? wave * 16 + r : wave * 32 + i * 16 + r) * (uint32_t)nblk + (uint32_t)(group * 16);
+                if (words && group * 16 + 16 <= nblk) {
+                    next_scale[i] = __builtin_amdgcn_raw_buffer_load_b128(src, (int)off, 0, 0);
+                } else {
 #pragma unroll
-                for (int c = 0; c < NT; ++c)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        red[wave][r][lane / 16 * 4 + q][c * 16 + lane % 16] = acc[r][c][q];
-            __syncthreads();
-            for (int o = threadIdx.x; o < NT * 256; o += kUpThreads) {
-                const int ri = o % 16, col = o / 16;
-                if (c0 + col < n && i0 + ri < a.I) {
-                    float g = 0.0f, u = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < kUpWaves; ++w) {
-                        g += red[w][0][ri][col];
-                        u += red[w][1][ri][col];
-                    }
-                    split_store<P>(h + (int64_t)l.ent[first + c0 + col] * a.I + i0 + ri, part,
-                                   silu_of(g) * u);
+                    for (int j = 0; j < kGroup; ++j)
+                        next_scale[i][j] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
+                                               src, (int)((off + 4 * j + g) | outside_if(group * 16 + 4 * j + g >= nblk)), 0, 0)
+                                           << (8 * g);
                 }
             }
-            __syncthreads();
-        };
-        int c0 = 0;
-        for (; c0 + 16 < n; c0 += kCols * 16) columns(std::integral_constant<int, kCols>{}, c0);
-        if (c0 < n) columns(std::integral_constant<int, 1>{}, c0);
-    }
-}
-
-template <bool MX, int P, bool F32>
-__global__ __launch_bounds__(kDownThreads) void down_kernel(DecodeArgs a, const Lists* lists,
-                                                            const uint16_t* h, int max_parts) {
-    __shared__ Lists l;
-    extern __shared__ __align__(16) float y[];     // [parts][N][16]
-    const int N = (int)(a.T * a.K);
-    for (int i = threadIdx.x; i < (int)(sizeof(Lists) / 4); i += kDownThreads)
-        ((uint32_t*)&l)[i] = ((const uint32_t*)lists)[i];
-    __syncthreads();
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int64_t part = (int64_t)N * a.I;
-    int parts = l.n > 0 ? (kDownWaves + l.n - 1) / l.n : 1;
-    if (parts > max_parts) parts = max_parts;
-    const int64_t h0 = (int64_t)blockIdx.x * 16;
-    int64_t hr = h0 + lane % 16;
-    if (hr >= a.H) hr = a.H - 1;
-    for (int item = wave; item < l.n * parts; item += kDownWaves) {
-        const int who = item / parts, p = item - who * parts;
-        const int e = l.ids[who], first = l.start[who], n = l.start[who + 1] - first;
-        const int64_t row[1] = {(int64_t)e * a.H + hr};
-        int k0, k1;
-        k_range<MX>(a.I, p, parts, k0, k1);
-        auto columns = [&](auto nt, int c0) {
-            constexpr int NT = decltype(nt)::value;
-            const uint16_t* b[NT];
-#pragma unroll
-            for (int c = 0; c < NT; ++c) {
-                int col = c0 + c * 16 + lane % 16;
-                if (col >= n) col = n - 1;
-                b[c] = h + (int64_t)l.ent[first + col] * a.I;
-            }
-            f32x4 acc[1][NT] = {};
-            stream<MX, 1, NT, P>(acc, a.w2, a.s2, row, a.I, b, part, k0, k1);
-#pragma unroll
-            for (int c = 0; c < NT; ++c) {
-                const int col = c0 + c * 16 + lane % 16;
-                if (col < n)
-                    *(f32x4*)(y + ((int64_t)p * N + l.ent[first + col]) * 16 + lane / 16 * 4) = acc[0][c];
-            }
-        };
-        int c0 = 0;
-        for (; c0 + 16 < n; c0 += kCols * 16) columns(std::integral_constant<int, kCols>{}, c0);
-        if (c0 < n) columns(std::integral_constant<int, 1>{}, c0);
-    }
-    __syncthreads();
-    for (int o = threadIdx.x; o < (int)a.T * 16; o += kDownThreads) {
-        const int t = o / 16, ri = o % 16;
-        if (h0 + ri >= a.H) continue;
-        float v = 0.0f;
-        for (int k = 0; k < a.K; ++k) {
-            const int f = t * a.K + k;
-            const int e = a.idx[f];
-            if (e < 0 || e >= a.E) continue;
-            float s = y[f * 16 + ri];
-            for (int p = 1; p < parts; ++p) s += y[((int64_t)p * N + f) * 16 + ri];
-            v += a.w[f] * s;
         }
-        const int64_t at = (int64_t)t * a.H + h0 + ri;
-        if constexpr (F32) {
-            ((float*)a.out)[at] = v;
+    };
+
+    f32x4 acc[2][NT];
+    auto clear = [&] {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < NT; ++c) acc[i][c] = f32x4{0, 0, 0, 0};
+    };
+    u32x4 scale[2] = {};
+    bool nan[2] = {};     // whether the lane has met the NaN scale in its row
+    auto use_stage = [&](const uint8_t* lds, int stage) {
+        const uint8_t* wa = lds + wave * 32 * S::kRowBytes + r * S::kRowBytes;
+        const uint8_t* wb = lds + S::kW + r * S::kColChunks * 16;
+        auto other = [&](int p, int c, int chunk) {
+            return as_bf16(ld16(wb + p * S::kPart + c * 16 * S::kColChunks * 16 + ((chunk ^ (r % 8)) * 16)));
+        };
+        if constexpr (MX) {
+            u32x4 codes[2];
+            float f[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                codes[i] = ld16(wa + i * 16 * S::kRowBytes + ((g ^ (r / 2 % 4)) * 16));
+                const uint32_t e = scale[i][stage] >> (8 * g) & 0xffu;
+                nan[i] |= e == 0xffu;
+                f[i] = __builtin_bit_cast(float, e << 23);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                bf16x8 w[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) w[i] = as_bf16(widen8(codes[i][q], f[i]));
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+#pragma unroll
+                    for (int c = 0; c < NT; ++c) {
+                        const bf16x8 b = other(p, c, 4 * g + q);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], b, acc[i][c], 0, 0, 0);
+                    }
+            }
         } else {
-            const __bf16 b = (__bf16)v;
-            ((uint16_t*)a.out)[at] = __builtin_bit_cast(uint16_t, b);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                bf16x8 w[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    w[i] = as_bf16(ld16(wa + i * 16 * S::kRowBytes + (((4 * q + g) ^ (r % 8)) * 16)));
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+#pragma unroll
+                    for (int c = 0; c < NT; ++c) {
+                        const bf16x8 b = other(p, c, 4 * q + g);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], b, acc[i][c], 0, 0, 0);
+                    }
+            }
         }
+    };
+    // A lane holds 4 consecutive output rows of one entry.
+    auto store_item = [&](int item) {
+        int slot;
+        const int64_t r0 = item_rows(item, slot);
+        const int first = l.first[slot], n = l.first[slot + 1] - first;
+        if constexpr (MX) {
+            // a NaN scale makes its whole row NaN; bit r of bad: row r
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint64_t bad = ballot64(nan[i]);
+                bad |= bad >> 32;
+                bad |= bad >> 16;
+                nan[i] = false;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (bad >> (4 * g + q) & 1)
+#pragma unroll
+                        for (int c = 0; c < NT; ++c) acc[i][c][q] = __builtin_nanf("");
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            const int col = c * 16 + r;
+            const int f = l.ent[first + (col < n ? col : 0)];
+            if constexpr (UP) {
+                const int64_t i = r0 + wave * 16 + 4 * g;
+                float v[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = silu_of(acc[0][c][q]) * acc[1][c][q];
+                for (int p = 0; p < h_parts; ++p) {
+                    const u32x2 b = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    if (col < n && i < M) *(u32x2*)(h + p * h_part + f * a.I + i) = b;
+                    const float was[4] = {bf16lo(b[0]), bf16hi(b[0]), bf16lo(b[1]), bf16hi(b[1])};
+                    // an infinity or a NaN stands in the first part alone
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] = __builtin_isfinite(v[q]) ? v[q] - was[q] : 0.0f;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int64_t row = r0 + wave * 32 + i * 16 + 4 * g;
+                    if (col < n && row < M) *(f32x4*)(y + f * a.H + row) = acc[i][c];
+                }
+            }
+        }
+        clear();
+    };
+
+    // All but the last `flying` loads of every wave have landed, and every wave's LDS reads
+    // are in registers.  The empty asm keeps the compiler from moving memory accesses over
+    // the barrier.
+    auto sync = [](auto flying) {
+        constexpr int F = decltype(flying)::value;
+        static_assert(F < 64, "vmcnt");
+        asm volatile("" ::: "memory");
+        // simm16 of s_waitcnt: vmcnt in bits 3:0 and 15:14, expcnt 6:4 (none), lgkmcnt 11:8 (0)
+        __builtin_amdgcn_s_waitcnt((F & 15) | (F >> 4) << 14 | 0x70);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr std::integral_constant<int, 2 * S::kLoads> two_stages{};
+
+    int item = blockIdx.x;
+    if (item >= items) return;
+    __syncthreads();      // the lists are done with their scratch
+    Cursor<S::kLoadsB> now, next;
+    seek(item, now);
+    clear();
+    load_scales(now, 0);
+    load_stage(lds0, now, 0);
+    load_stage(lds1, now, 1);
+    load_stage(lds2, now, 2);
+    for (int group = 0;;) {
+        // where the stream goes after this group; behind the last item it loads zeros
+        const bool last = group + 1 == groups;
+        const int next_item = last ? item + (int)gridDim.x : item;
+        const int next_group = last ? 0 : group + 1;
+        const bool more = next_item < items;
+        next = now;
+        if (last && more) seek(next_item, next);
+        const int beyond = more ? 0 : 1 << 20;
+        scale[0] = next_scale[0];
+        scale[1] = next_scale[1];
+        if (more) load_scales(next, next_group);
+        sync(two_stages);
+        load_stage(lds3, now, group * kGroup + 3);
+        use_stage(lds0, 0);
+        sync(two_stages);
+        load_stage(lds0, next, next_group * kGroup + beyond);
+        use_stage(lds1, 1);
+        sync(two_stages);
+        load_stage(lds1, next, next_group * kGroup + 1 + beyond);
+        use_stage(lds2, 2);
+        sync(two_stages);
+        load_stage(lds2, next, next_group * kGroup + 2 + beyond);
+        use_stage(lds3, 3);
+        if (last) store_item(item);
+        if (!more) break;
+        item = next_item;
+        group = next_group;
+        now = next;
     }
+    // no load into LDS may be in flight when it goes to the next workgroup
+    __builtin_amdgcn_s_waitcnt(0);
 }
 
-constexpr size_t kListBytes = (sizeof(Lists) + 255) / 256 * 256;
-static_assert(sizeof(Lists) % 4 == 0, "copied by words");
+// out[t] = sum over k, ascending, of w[t,k] * y[t*K + k].
+constexpr int kJoinThreads = 256;
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(DecodeArgs a, const float* y) {
+    const int64_t t = blockIdx.y;
+    const int64_t c = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x) * 4;
+    if (c >= a.H) return;
+    float v[4] = {0, 0, 0, 0};
+    for (int k = 0; k < a.K; ++k) {
+        const int64_t f = t * a.K + k;
+        const int e = a.idx[f];
+        if (e < 0 || e >= a.E) continue;
+        const f32x4 z = *(const f32x4*)(y + f * a.H + c);
+        const float w = a.w[f];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] += w * z[q];
+    }
+    if (a.out_f32) store_unit<true, false>(a.out, t * a.H + c, v);
+    else store_unit<false, false>(a.out, t * a.H + c, v);
+}
 
-template <bool MX, int P, bool F32>
-hipError_t launch(const DecodeArgs& a, hipStream_t s) {
+// Workgroups: as many as fit the card at once (LDS decides), or one per item.
+template <bool MX, bool UP, int P, int NT, int WAVES>
+hipError_t launch(const DecodeArgs& a, Lists* lists, uint16_t* h, int64_t h_part, float* y, int parts,
+                  hipStream_t s) {
+    using S = Stream<MX, UP, P, NT, WAVES>;
+    const int64_t N = a.T * a.K, M = UP ? a.I : a.H, K = UP ? a.H : a.I;
+    const int64_t most = N * ((M + S::kRows - 1) / S::kRows);
+    const int per_cu = (int)(kLdsPerCu / (kGroup * S::kStageBytes + sizeof(Lists)));
+    const int64_t fit = (int64_t)256 * (per_cu < 1 ? 1 : per_cu);
+    const uintptr_t sp = (uintptr_t)(UP ? a.s13 : a.s2);
+    const int words = MX && K / 32 % 4 == 0 && sp % 4 == 0;
+    stream_kernel<MX, UP, P, NT, WAVES><<<dim3((unsigned)(most < fit ? most : fit)), S::kThreads, 0, s>>>(
+        a, lists, h, h_part, y, parts, words);
+    return hipGetLastError();
+}
+
+template <bool MX, bool UP, int P, int NT>
+hipError_t launch_waves(const DecodeArgs& a, Lists* lists, uint16_t* h, int64_t h_part, float* y,
+                        int parts, hipStream_t s) {
+    const int64_t N = a.T * a.K, used = N < a.E ? N : a.E, M = UP ? a.I : a.H;
+    // 4 waves share the entries' rows; 2 where 4 would leave CUs without work
+    if (used * ((M + (UP ? 63 : 127)) / (UP ? 64 : 128)) >= 512)
+        return launch<MX, UP, P, NT, 4>(a, lists, h, h_part, y, parts, s);
+    return launch<MX, UP, P, NT, 2>(a, lists, h, h_part, y, parts, s);
+}
+
+template <bool MX, int P, int NT>
+hipError_t launch_all(const DecodeArgs& a, hipStream_t s) {
     const int64_t N = a.T * a.K;
     Lists* lists = (Lists*)a.ws;
-    uint16_t* h = (uint16_t*)((char*)a.ws + kListBytes);
-    const int64_t most = (N < a.E ? N : a.E) * ((a.I + 15) / 16);
-    up_kernel<MX, P><<<dim3((unsigned)(most < 2048 ? most : 2048)), kUpThreads, 0, s>>>(a, lists, h);
-    const int max_parts = (int)(kMaxEntries / N < kDownWaves ? kMaxEntries / N : kDownWaves);
-    const size_t lds = (size_t)max_parts * N * 16 * sizeof(float);
-    down_kernel<MX, P, F32><<<dim3((unsigned)((a.H + 15) / 16)), kDownThreads, lds, s>>>(a, lists, h,
-                                                                                        max_parts);
+    float* y = (float*)((char*)a.ws + kListBytes);
+    uint16_t* h = (uint16_t*)(y + N * a.H);
+    const int64_t h_part = N * a.I;
+    hipError_t st = launch_waves<MX, true, 1, NT>(a, lists, h, h_part, y, P, s);
+    if (st == hipSuccess) st = launch_waves<MX, false, P, NT>(a, lists, h, h_part, y, P, s);
+    if (st != hipSuccess) return st;
+    const dim3 grid((unsigned)((a.H + 4 * kJoinThreads - 1) / (4 * kJoinThreads)), (unsigned)a.T);
+    join_kernel<<<grid, kJoinThreads, 0, s>>>(a, y);
     return hipGetLastError();
 }
 
 template <bool MX>
-hipError_t launch(const DecodeArgs& a, hipStream_t s) {
-    return a.out_f32 ? launch<MX, 3, true>(a, s) : launch<MX, 2, false>(a, s);
+hipError_t launch_type(const DecodeArgs& a, hipStream_t s) {
+    // entries of an expert on average: 16 of them are worked on at once, or 32
+    const bool wide = a.T * a.K > 8 * (int64_t)a.E;
+    if (a.out_f32) return wide ? launch_all<MX, 3, 2>(a, s) : launch_all<MX, 3, 1>(a, s);
+    return wide ? launch_all<MX, 2, 2>(a, s) : launch_all<MX, 2, 1>(a, s);
 }
 
 }  // namespace
 
-size_t decode_ws(int64_t T, int K, int64_t I) {
-    return kListBytes + (size_t)(T * K) * I * 3 * sizeof(uint16_t);
+size_t decode_ws(int64_t T, int K, int64_t H, int64_t I) {
+    return kListBytes + (size_t)(T * K) * ((size_t)H * sizeof(float) + (size_t)I * 3 * sizeof(uint16_t));
 }
 
 hipError_t launch_experts_decode(const DecodeArgs& a, hipStream_t s) {
     if (a.T == 0) return hipSuccess;
-    return a.s13 ? launch<true>(a, s) : launch<false>(a, s);
+    return a.s13 ? launch_type<true>(a, s) : launch_type<false>(a, s);
 }
 
 }  // namespace moe

@@ -68,13 +68,14 @@ int moe_expert_product_mxfp4(const void* a, const void* a_scales, int64_t rows, 
                              int swiglu, void* y, moe_dtype y_dt, void* stream);
 
 /* Bytes of device workspace that moe_experts_decode needs for these sizes (0 for sizes
- * outside its limits).  It does not shrink when T, K or I grows, needs no initialisation
- * and may be reused by consecutive calls on one stream, also from a captured graph.
+ * outside its limits).  It does not shrink when T, K, H or I grows, so one for the largest
+ * sizes serves all; it needs no initialisation and may be reused by consecutive calls on
+ * one stream, also from a captured graph.
  * Calls that may run at the same time need workspaces of their own. */
-size_t moe_experts_decode_workspace_size(int64_t T, int K, int64_t I);
+size_t moe_experts_decode_workspace_size(int64_t T, int K, int64_t H, int64_t I);
 
-/* The whole experts' step of a few tokens (T*K <= 1024), from token rows to token rows,
- * in two kernels, without a dispatch or a combine:
+/* The whole experts' step of a few tokens (T*K <= 1024; H, I <= 2^20), from token rows to
+ * token rows, without a dispatch or a combine:
  *   out[t] = sum over k of w[t,k] * W2[e] h,  h = silu(W1[e] x[t]) * (W3[e] x[t]),  e = idx[t,k]
  * The sum over k ascends, in f32; entries whose idx is outside [0,E) are skipped whatever
  * their w holds, and a token without any other gets zeros.  h is held between the
@@ -87,7 +88,7 @@ size_t moe_experts_decode_workspace_size(int64_t T, int K, int64_t I);
  *           infinite
  *   w2      [E,H,I], likewise, with w2_scales [E,H,I/32]; both scales NULL for bf16
  *   out     out [T,H] out_dt (MOE_BF16 or MOE_F32)
- *   ws      at least moe_experts_decode_workspace_size(T, K, I) bytes, 256-byte aligned */
+ *   ws      at least moe_experts_decode_workspace_size(T, K, H, I) bytes, 256-byte aligned */
 int moe_experts_decode(const void* x, int64_t T, int64_t H, const int32_t* idx, const float* w,
                        int K, int E, int64_t I, const void* w13, const void* w13_scales,
                        const void* w2, const void* w2_scales, moe_dtype wt_dt, void* out,

@@ -100,13 +100,13 @@ res["swiglu_backward"] = {
     "pc_alone": sb(po=None), "in_place": sb(dgu=B["gu"]), "dgu_on_dh": sb(dgu=B["dh"]),
     "h_on_dh": sb(h=B["dh"]), "h_on_dgu": sb(h=B["dgu"]), "dgu_on_sc": sb(dgu=B["sc"]),
 }
-need = lib.moe_experts_decode_workspace_size(5, 4, 32)
+need = lib.moe_experts_decode_workspace_size(5, 4, 64, 32)
 de = case(lib.moe_experts_decode, "x T H idx w K E I w13 s13 w2 s2 wdt out odt ws n".split(),
           dict(x=B["x"], T=5, H=64, idx=B["idx"], w=B["wt"], K=4, E=8, I=32, w13=B["w13"], s13=B["s13"],
                w2=B["w2"], s2=B["s2"], wdt=3, out=B["out"], odt=0, ws=B["ws"], n=need))
 res["experts_decode"] = {
     "odt": de(odt=2), "wdt_f32": de(wdt=1), "wdt_fp8": de(wdt=2), "H40": de(H=40), "I40": de(I=40),
-    "H12_bf16": de(H=12, wdt=0, s13=None, s2=None), "H0": de(H=0), "I_huge": de(I=(1 << 24) + 32),
+    "H12_bf16": de(H=12, wdt=0, s13=None, s2=None), "H0": de(H=0), "I_huge": de(I=(1 << 20) + 32), "H_huge": de(H=(1 << 20) + 32),
     "K0": de(K=0), "K17": de(K=17), "Tneg": de(T=-1), "TK1025": de(T=1025, K=1), "TK_over": de(T=65, K=16),
     "Thuge": de(T=1 << 62), "E0": de(E=0), "E1025": de(E=1025), "x_null": de(x=None), "x_odd": de(x=B["x"] + 8),
     "idx_null": de(idx=None), "idx_odd": de(idx=B["idx"] + 2), "w_null": de(w=None), "w_odd": de(w=B["wt"] + 1),
@@ -119,11 +119,13 @@ res["experts_decode"] = {
 }
 res["decode_ws"] = {"null": de(ws=None), "small": de(n=need - 1), "odd": de(ws=B["ws"] + 128)}
 size = lib.moe_experts_decode_workspace_size
-res["grows"] = all(size(T, K, I) <= size(T + 1, K, I) <= size(T + 1, K + 1, I) <= size(T + 1, K + 1, I + 8)
-                   for T in (0, 1, 31, 59) for K in (1, 7, 15) for I in (8, 2048))
-res["no_size"] = [size(-1, 1, 8), size(1025, 1, 8), size(65, 16, 8), size(1, 0, 8), size(1, 17, 8),
-                  size(1, 1, 0), size(1, 1, 12), size(1, 1, (1 << 24) + 8), size(1 << 62, 16, 8)]
-n, E4 = None, dict(pc=B["pc"], po=B["po"])
+res["grows"] = all(size(T, K, H, I) <= size(T + 1, K, H, I) <= size(T + 1, K + 1, H, I)
+                   <= size(T + 1, K + 1, H + 8, I) <= size(T + 1, K + 1, H + 8, I + 8)
+                   for T in (0, 1, 31, 59) for K in (1, 7, 15) for H in (8, 4096) for I in (8, 2048))
+res["no_size"] = [size(-1, 1, 8, 8), size(1025, 1, 8, 8), size(65, 16, 8, 8), size(1, 0, 8, 8),
+                  size(1, 17, 8, 8), size(1, 1, 8, 0), size(1, 1, 8, 12), size(1, 1, 12, 8),
+                  size(1, 1, 8, (1 << 20) + 8), size(1, 1, (1 << 20) + 8, 8), size(1 << 62, 16, 8, 8)]
+n = None
 res["empty"] = [q(rows=0, x=n, q=n, s=n)[0], dq(rows=0, q=n, s=n, y=n)[0],
                 pr(rows=0, a=n, sa=n, y=n)[0], sw(rows=0, gu=n, h=n)[0],
                 sb(rows=0, dh=n, gu=n, sc=n, dgu=n)[0], de(T=0, x=n, idx=n, w=n, out=n)[0]]

@@ -41,19 +41,20 @@ constexpr int kMaxEntries = kDecodeEntries;
 constexpr int kGroup = 4;      // stages in LDS
 
 // The work of one pass over an expert's weights: up to `width` of its entries.  Slot s
-// belongs to expert[s] and has the entries ent[first[s]] .. ent[first[s + 1] - 1].
+// belongs to expert[s] and has the entries ent[first[s]] .. ent[first[s + 1] - 1].  All
+// three are arrays of one block of 16-bit words, sized by the number of entries, so that
+// few entries leave the LDS to the stages.
 struct Lists {
-    int n;
-    uint16_t expert[kMaxEntries];
-    uint16_t first[kMaxEntries + 2];
-    uint16_t ent[kMaxEntries];
+    uint16_t *n, *expert, *first, *ent;
+    __device__ __forceinline__ Lists(uint16_t* base, int N)
+        : n(base), expert(base + 2), first(base + 2 + N), ent(base + 4 + 2 * N) {}
 };
-static_assert(sizeof(Lists) % 4 == 0, "copied by words");
-constexpr size_t kListBytes = (sizeof(Lists) + 255) / 256 * 256;
+__host__ __device__ constexpr int list_words(int64_t N) { return (int)(4 + 3 * N + 1) / 2; }   // of 32 bits
+constexpr size_t kListBytes = (list_words(kMaxEntries) * 4 + 255) / 256 * 256;
 
 // Builds the lists from the ids, by the whole workgroup.  cnt and sum are scratch.
 template <int THREADS>
-__device__ void build_lists(const int32_t* idx, int N, int E, int width, Lists& l,
+__device__ void build_lists(const int32_t* idx, int N, int E, int width, const Lists& l,
                             int (&cnt)[1024], int (&sum)[THREADS / kWave][2]) {
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     for (int e = tid; e < E; e += THREADS) cnt[e] = 0;
@@ -113,7 +114,7 @@ __device__ void build_lists(const int32_t* idx, int N, int E, int width, Lists& 
         at += c;
     }
     if (tid == 0) {
-        l.n = all;
+        *l.n = (uint16_t)all;
         l.first[all] = (uint16_t)entries;
     }
     __syncthreads();
@@ -201,15 +202,16 @@ struct Cursor {
 };
 
 template <bool MX, bool UP, int P, int NT, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, Lists* lists,
+__global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uint32_t* lists,
                                                                uint16_t* h, int64_t h_part,
                                                                float* y, int h_parts, int words) {
     using S = Stream<MX, UP, P, NT, WAVES>;
     constexpr int kThreads = S::kThreads;
-    __shared__ Lists l;
+    extern __shared__ __align__(16) uint32_t list_block[];
     __shared__ __align__(16) uint8_t lds0[S::kStageBytes], lds1[S::kStageBytes];
     __shared__ __align__(16) uint8_t lds2[S::kStageBytes], lds3[S::kStageBytes];
     const int N = (int)(a.T * a.K);
+    const Lists l((uint16_t*)list_block, N);
     if constexpr (UP) {
         // the scratch of the lists is in the stages' space, which is not in use yet
         static_assert(sizeof(int[1024]) <= S::kStageBytes, "scratch");
@@ -217,18 +219,16 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, Lis
         int(&sum)[WAVES][2] = *reinterpret_cast<int(*)[WAVES][2]>(lds1);
         build_lists<kThreads>(a.idx, N, a.E, 16 * NT, l, cnt, sum);
         if (blockIdx.x == 0)
-            for (int i = threadIdx.x; i < (int)(sizeof(Lists) / 4); i += kThreads)
-                ((uint32_t*)lists)[i] = ((const uint32_t*)&l)[i];
+            for (int i = threadIdx.x; i < list_words(N); i += kThreads) lists[i] = list_block[i];
     } else {
-        for (int i = threadIdx.x; i < (int)(sizeof(Lists) / 4); i += kThreads)
-            ((uint32_t*)&l)[i] = ((const uint32_t*)lists)[i];
+        for (int i = threadIdx.x; i < list_words(N); i += kThreads) list_block[i] = lists[i];
         __syncthreads();
     }
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t K = UP ? a.H : a.I, M = UP ? a.I : a.H;     // sum length, output rows of an expert
     const int blocks = (int)((M + S::kRows - 1) / S::kRows);
-    const int items = __builtin_amdgcn_readfirstlane(l.n) * blocks;
+    const int items = __builtin_amdgcn_readfirstlane((int)*l.n) * blocks;
     const int chunks = (int)(MX ? K / 32 : K / 8), col_chunks = (int)(K / 8);
     const int groups = (int)((K + S::kStageK * kGroup - 1) / (S::kStageK * kGroup));
     const int64_t rb = MX ? K / 2 : K * 2, wrows = UP ? 2 * M : M;
@@ -240,9 +240,9 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, Lis
     auto seek = [&](int item, Cursor<S::kLoadsB>& c) {
         int slot;
         const int64_t r0 = item_rows(item, slot);
-        const int e = __builtin_amdgcn_readfirstlane(l.expert[slot]);
-        const int first = __builtin_amdgcn_readfirstlane(l.first[slot]);
-        const int n = __builtin_amdgcn_readfirstlane(l.first[slot + 1]) - first;
+        const int e = __builtin_amdgcn_readfirstlane((int)l.expert[slot]);
+        const int first = __builtin_amdgcn_readfirstlane((int)l.first[slot]);
+        const int n = __builtin_amdgcn_readfirstlane((int)l.first[slot + 1]) - first;
         c.row = (int64_t)e * wrows + r0;
         c.rows = (int)(M - r0 < S::kRows ? M - r0 : S::kRows);
 #pragma unroll
@@ -474,15 +474,27 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(DecodeArgs a, const 
     const int64_t t = blockIdx.y;
     const int64_t c = ((int64_t)blockIdx.x * kJoinThreads + threadIdx.x) * 4;
     if (c >= a.H) return;
+    // (the rows of half the largest K are loaded together; a row that no expert has written
+    // is read as well, and not used)
     float v[4] = {0, 0, 0, 0};
-    for (int k = 0; k < a.K; ++k) {
-        const int64_t f = t * a.K + k;
-        const int e = a.idx[f];
-        if (e < 0 || e >= a.E) continue;
-        const f32x4 z = *(const f32x4*)(y + f * a.H + c);
-        const float w = a.w[f];
+    constexpr int kBatch = 8;
+    for (int k0 = 0; k0 < a.K; k0 += kBatch) {
+        f32x4 z[kBatch];
+        float w[kBatch];
+        bool has[kBatch];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] += w * z[q];
+        for (int j = 0; j < kBatch; ++j) {
+            const int64_t f = t * a.K + (k0 + j < a.K ? k0 + j : 0);
+            const int e = a.idx[f];
+            has[j] = k0 + j < a.K && e >= 0 && e < a.E;
+            w[j] = a.w[f];
+            z[j] = *(const f32x4*)(y + f * a.H + c);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (has[j])
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] += w[j] * z[j][q];
     }
     if (a.out_f32) store_unit<true, false>(a.out, t * a.H + c, v);
     else store_unit<false, false>(a.out, t * a.H + c, v);
@@ -490,22 +502,23 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(DecodeArgs a, const 
 
 // Workgroups: as many as fit the card at once (LDS decides), or one per item.
 template <bool MX, bool UP, int P, int NT, int WAVES>
-hipError_t launch(const DecodeArgs& a, Lists* lists, uint16_t* h, int64_t h_part, float* y, int parts,
+hipError_t launch(const DecodeArgs& a, uint32_t* lists, uint16_t* h, int64_t h_part, float* y, int parts,
                   hipStream_t s) {
     using S = Stream<MX, UP, P, NT, WAVES>;
     const int64_t N = a.T * a.K, M = UP ? a.I : a.H, K = UP ? a.H : a.I;
     const int64_t most = N * ((M + S::kRows - 1) / S::kRows);
-    const int per_cu = (int)(kLdsPerCu / (kGroup * S::kStageBytes + sizeof(Lists)));
+    const size_t lists_lds = (size_t)list_words(N) * 4;
+    const int per_cu = (int)(kLdsPerCu / (kGroup * S::kStageBytes + lists_lds));
     const int64_t fit = (int64_t)256 * (per_cu < 1 ? 1 : per_cu);
     const uintptr_t sp = (uintptr_t)(UP ? a.s13 : a.s2);
     const int words = MX && K / 32 % 4 == 0 && sp % 4 == 0;
-    stream_kernel<MX, UP, P, NT, WAVES><<<dim3((unsigned)(most < fit ? most : fit)), S::kThreads, 0, s>>>(
+    stream_kernel<MX, UP, P, NT, WAVES><<<dim3((unsigned)(most < fit ? most : fit)), S::kThreads, lists_lds, s>>>(
         a, lists, h, h_part, y, parts, words);
     return hipGetLastError();
 }
 
 template <bool MX, bool UP, int P, int NT>
-hipError_t launch_waves(const DecodeArgs& a, Lists* lists, uint16_t* h, int64_t h_part, float* y,
+hipError_t launch_waves(const DecodeArgs& a, uint32_t* lists, uint16_t* h, int64_t h_part, float* y,
                         int parts, hipStream_t s) {
     const int64_t N = a.T * a.K, used = N < a.E ? N : a.E, M = UP ? a.I : a.H;
     // 4 waves share the entries' rows; 2 where 4 would leave CUs without work
@@ -517,7 +530,7 @@ hipError_t launch_waves(const DecodeArgs& a, Lists* lists, uint16_t* h, int64_t 
 template <bool MX, int P, int NT>
 hipError_t launch_all(const DecodeArgs& a, hipStream_t s) {
     const int64_t N = a.T * a.K;
-    Lists* lists = (Lists*)a.ws;
+    uint32_t* lists = (uint32_t*)a.ws;
     float* y = (float*)((char*)a.ws + kListBytes);
     uint16_t* h = (uint16_t*)(y + N * a.H);
     const int64_t h_part = N * a.I;

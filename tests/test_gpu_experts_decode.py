@@ -131,6 +131,25 @@ def test_odd_sizes_in_bf16(H, I, out):
     _check(y, _ref(x.double(), idx, w, w13[2], w2[2], 3 if out == F32 else 2), "odd")
 
 
+@pytest.mark.parametrize("T,H,I,E,K", [(14, 3040, 352, 6, 4), (1, 672, 1984, 18, 2), (9, 992, 2080, 3, 1)])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_scale_rows_at_any_byte(T, H, I, E, K, out):
+    """Rows of 95, 11, 21, 62, 31 and 65 scales, read 16 bytes at a time."""
+    note(f"decode scales T={T} H={H} I={I}")
+    x, idx, w, w13, w2 = _inputs(T, H, I, E, K, True, H + I)
+    y = _call(x, idx, w, w13, w2, out)
+    _check(y, _ref(x.double(), idx, w, w13[2], w2[2], 3 if out == F32 else 2), "scales")
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T,E,K", [(1024, 1024, 1), (64, 5, 16), (1024, 1, 1)])
+def test_as_many_entries_as_are_allowed(T, E, K, mx):
+    note(f"decode full T={T} E={E} K={K} mx={mx}")
+    x, idx, w, w13, w2 = _inputs(T, 64, 32, E, K, mx, T + E, none=0.0)
+    y = _call(x, idx, w, w13, w2, F32)
+    _check(y, _ref(x.double(), idx, w, w13[2], w2[2], 3), "full")
+
+
 @pytest.mark.parametrize("mx", [False, True])
 def test_entries_that_count_for_nothing(mx):
     """Ids outside the experts with weights that must not be read as numbers, an expert named

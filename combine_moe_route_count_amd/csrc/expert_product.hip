@@ -7,19 +7,26 @@
 // Weights are its rows and activations its columns, so a lane ends up with 4
 // consecutive n of one row.
 //
-// A workgroup of 4 waves owns BM rows of one expert and 256 weight rows (with SwiGLU
-// 128 gate and 128 up rows, 32 of each in turn, so a lane holds both halves of its
+// A workgroup of 4 waves owns BM rows (64, 128 or 256) of one expert and 256 weight rows (with
+// SwiGLU 128 gate and 128 up rows, 32 of each in turn, so a lane holds both halves of its
 // outputs).  Which expert a workgroup has follows from packed_cnt on the device; the
-// grid covers the most tiles that the row count allows, and the rest leave at once.
+// grid covers the most tiles that the row count allows, and the rest leave at once.  A tile
+// of at most BM / 2 rows runs at half the height.  Where there are few tiles, others of 32
+// rows and 64 weight rows take over, whose 4 waves share out K and add their sums in LDS.
 //
-// K runs in stages of 256 elements: 128 bytes of each row, loaded straight into LDS
-// while the stage before is multiplied.  The 16-byte chunks of a row are stored at
-// (chunk ^ row % 8), so that 8 lanes that read one chunk of 8 rows meet different
-// banks.  A stage is four matrix steps; lane half g takes chunks 4g to 4g+3, which puts
-// its four scales side by side in memory.  Fragments are read one step ahead of the
-// matrix instructions, so one barrier a stage is enough: before the last step every wave
-// holds the rest of the stage in registers, its LDS is free for the stage after next,
-// and the next stage has landed.
+// K runs in stages of 128 elements: 64 bytes of each row, loaded straight into LDS, four
+// stages deep, so that three are in flight while one is multiplied.  The 16-byte chunks of a
+// row are stored at (chunk ^ row / 2 % 4), so that 8 lanes that read one chunk of 8 rows meet
+// different banks.  A stage is two matrix steps of 64 elements, of which lane half g takes
+// chunk g.  The body of a stage is one block without a branch: with one the compiler moves
+// the matrix instructions behind it, away from the loads they were to cover.
+//
+// Scales are loaded for four stages at once, one 16-byte load per row where rows start at whole
+// words: loads of single words kept the address unit busier than the matrix cores.
+//
+// Measured on rows of random codes: 2.9e15 operations a second (32768 rows x 4096 x 7168 over
+// 64 experts, SwiGLU), 3.6e15 (8192 x 8192 x 8192), where the matrix instruction alone runs at
+// 6.3e15; 5.6 TB/s of weights where experts have two rows each (128 experts, 4096 x 4096).
 //
 // Rows behind a segment, weight rows behind N and chunks behind H are loaded as zeros
 // by the range check of the buffer descriptors (their scales too, so a NaN scale of a
@@ -688,13 +695,23 @@ hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
     // Tile heights 64, 128, 256 by the mean rows of an expert, in us (32 experts with uneven
     // loads, 4096 x 4096): mean 24 62, 64, 72; 64 73, 75, 82; 96 91, 90, 94; 192 135, 117, 122;
     // 256 163, 148, 128; 384 224, 200, 185.
-    // Narrow tiles against tiles of 64 rows, in us, by the number of the latter (mean rows 1 to
-    // 40): 8 tiles 8.1, 10.4; 32 14.5, 23.2; 64 11.5, 15.1; 128 17.1, 15.6; 256 30.5, 21.2.
+    // A height whose tiles would leave 100 CUs without one gives way to the next lower, in us:
+    // 120 tiles of 256 rows 22.2 against 16.9 with 128, 136 35.7 and 28.4, 168 23.6 and 27.6,
+    // 184 37.3 and 44.9; 138 tiles of 128 rows 22.5 against 20.2 with 64, 144 22.8 and 20.8,
+    // 184 24.9 and 31.2, 192 26.4 and 31.9.
+    // Narrow tiles where nearly each can have a CU, in us against tiles of 64 rows: 56 of them 9.0
+    // and 17.8, 160 11.6 and 16.1, 256 17.9 and 27.6, 264 17.2 and 27.2; 320 20.3 and 16.4,
+    // 512 31.5 and 27.8.
+    const int64_t used = a.E < a.rows ? a.E : a.rows;
+    auto tiles = [&](int64_t height, int64_t width) {       // about
+        const int64_t row_tiles = (2 * a.rows / height + used) / 2;
+        return (row_tiles > used ? row_tiles : used) * ((a.N + width - 1) / width);
+    };
+    constexpr int64_t kCUs = 256, kIdle = 100;
     const int64_t mean = a.rows / a.E;
-    const int64_t wide = (a.E < a.rows ? a.E : a.rows) * ((a.N + kBN - 1) / kBN);
-    if (mean <= 40 && wide < 96) MOE_PRODUCT(kNarrowRows, kNarrowBN, product_narrow_kernel);
-    else if (mean <= 64) MOE_PRODUCT(64, kBN, product_kernel, 64 MOE_COMMA);
-    else if (mean < 224) MOE_PRODUCT(128, kBN, product_kernel, 128 MOE_COMMA);
+    if (tiles(kNarrowRows, kNarrowBN) <= kCUs + kCUs / 8) MOE_PRODUCT(kNarrowRows, kNarrowBN, product_narrow_kernel);
+    else if (mean <= 64 || tiles(128, kBN) < kCUs - kIdle) MOE_PRODUCT(64, kBN, product_kernel, 64 MOE_COMMA);
+    else if (mean < 224 || tiles(256, kBN) < kCUs - kIdle) MOE_PRODUCT(128, kBN, product_kernel, 128 MOE_COMMA);
     else MOE_PRODUCT(256, kBN, product_kernel, 256 MOE_COMMA);
     return hipGetLastError();
 }

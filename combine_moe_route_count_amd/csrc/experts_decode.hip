@@ -36,6 +36,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 using Lds = __attribute__((address_space(3))) uint8_t;
+using LdsWords = __attribute__((address_space(3))) u32x4;
 
 constexpr int kMaxEntries = kDecodeEntries;
 constexpr int kGroup = 4;      // stages in LDS
@@ -52,30 +53,64 @@ struct Lists {
 __host__ __device__ constexpr int list_words(int64_t N) { return (int)(4 + 3 * N + 1) / 2; }   // of 32 bits
 constexpr size_t kListBytes = (list_words(kMaxEntries) * 4 + 255) / 256 * 256;
 
-// Builds the lists from the ids, by the whole workgroup.  cnt and sum are scratch.
+// Scratch of build_lists: how many entries of each expert a chunk of 64 entries has (16
+// chunks, 64 at the most), in four arrays of 256 experts each, and sums of the waves.
+struct ListScratch {
+    static constexpr int kChunks = kMaxEntries / kWave;
+    static constexpr int kExperts = 256;
+    Lds *count0, *count1, *count2, *count3;
+    int (*sum)[2];
+    __device__ __forceinline__ Lds* of(int e) const {
+        Lds* low = e < kExperts ? count0 : count1;
+        Lds* high = e < 3 * kExperts ? count2 : count3;
+        return (e < 2 * kExperts ? low : high) + e % kExperts * kChunks;
+    }
+};
+
+// Builds the lists from the ids, by the whole workgroup; entries of an expert in ascending
+// order, the same in every workgroup.  Each wave finds the ranks of entries in its chunks; where
+// a chunk's entries go follows from the counts of the chunks before it.
 template <int THREADS>
 __device__ void build_lists(const int32_t* idx, int N, int E, int width, const Lists& l,
-                            int (&cnt)[1024], int (&sum)[THREADS / kWave][2]) {
+                            const ListScratch& sc, uint16_t* start) {
+    constexpr int kWaves = THREADS / kWave, kPer = ListScratch::kChunks / kWaves;
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-    for (int e = tid; e < E; e += THREADS) cnt[e] = 0;
-    __syncthreads();
-    constexpr int kPer = kMaxEntries / THREADS;
+    int e[kPer], rank[kPer], same[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int f = tid + i * THREADS;
-        const int e = f < N ? idx[f] : -1;
-        if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
+        const int f = (i * kWaves + wave) * kWave + lane;
+        e[i] = f < N ? idx[f] : -1;
+        if (e[i] >= E || e[i] < 0) e[i] = -1;
+    }
+    for (int i = tid; i < E; i += THREADS) *(LdsWords*)sc.of(i) = u32x4{0, 0, 0, 0};
+    const int bits = E > 1 ? 32 - __builtin_clz(E - 1) : 1;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const uint64_t lanes = match_key(e[i], bits);
+        rank[i] = lanes_below(lanes);
+        same[i] = __popcll(lanes);
     }
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (e[i] >= 0 && rank[i] == 0) sc.of(e[i])[i * kWaves + wave] = (uint8_t)same[i];
+    __syncthreads();
+    auto entries = [](u32x4 v) {
+        uint32_t n = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n = __builtin_amdgcn_sad_u8(v[j], 0u, n);
+        return (int)n;
+    };
     // exclusive sums over the experts, of slots and of entries
     constexpr int kPerE = 1024 / THREADS;
-    int slots = 0, total = 0;
+    const int per = (E + THREADS - 1) / THREADS;       // experts of a thread
+    int cnt[kPerE], slots = 0, total = 0;
 #pragma unroll
     for (int i = 0; i < kPerE; ++i) {
-        const int e = tid * kPerE + i;
-        const int c = e < E ? cnt[e] : 0;
-        slots += (c + width - 1) / width;
-        total += c;
+        const int x = tid * per + i;
+        cnt[i] = i < per && x < E ? entries(*(const LdsWords*)sc.of(x)) : 0;
+        slots += (cnt[i] + width - 1) / width;
+        total += cnt[i];
     }
     int u = slots, t = total;
 #pragma unroll
@@ -87,55 +122,50 @@ __device__ void build_lists(const int32_t* idx, int N, int E, int width, const L
         }
     }
     if (lane == kWave - 1) {
-        sum[wave][0] = u;
-        sum[wave][1] = t;
+        sc.sum[wave][0] = u;
+        sc.sum[wave][1] = t;
     }
     __syncthreads();
-    int a = u - slots, at = t - total, all = 0, entries = 0;
+    int a = u - slots, at = t - total, all = 0, used = 0;
 #pragma unroll
-    for (int i = 0; i < THREADS / kWave; ++i) {
+    for (int i = 0; i < kWaves; ++i) {
         if (i < wave) {
-            a += sum[i][0];
-            at += sum[i][1];
+            a += sc.sum[i][0];
+            at += sc.sum[i][1];
         }
-        all += sum[i][0];
-        entries += sum[i][1];
+        all += sc.sum[i][0];
+        used += sc.sum[i][1];
     }
 #pragma unroll
     for (int i = 0; i < kPerE; ++i) {
-        const int e = tid * kPerE + i;
-        const int c = e < E ? cnt[e] : 0;
-        for (int j = 0; j < c; j += width) {
-            l.expert[a] = (uint16_t)e;
+        const int x = tid * per + i;
+        if (cnt[i] == 0) continue;
+        for (int j = 0; j < cnt[i]; j += width) {
+            l.expert[a] = (uint16_t)x;
             l.first[a] = (uint16_t)(at + j);
             ++a;
         }
-        if (e < E) cnt[e] = at;    // from here on: where the expert's next entry goes
-        at += c;
+        start[x] = (uint16_t)at;
+        at += cnt[i];
     }
     if (tid == 0) {
         *l.n = (uint16_t)all;
-        l.first[all] = (uint16_t)entries;
+        l.first[all] = (uint16_t)used;
     }
     __syncthreads();
-    // Entries to their places, 64 at a time, in ascending order: every workgroup has to find
-    // the same lists.
-    const int bits = E > 1 ? 32 - __builtin_clz(E - 1) : 1;
-    for (int c = 0; c * kWave < N; ++c) {
-        if (c % (THREADS / kWave) == wave) {
-            const int f = c * kWave + lane;
-            int e = f < N ? idx[f] : -1;
-            if (e >= E || e < 0) e = -1;
-            const uint64_t same = match_key(e, bits);
-            const int base = e >= 0 ? cnt[e] : 0, rank = lanes_below(same);
-            __builtin_amdgcn_wave_barrier();
-            if (e >= 0) {
-                l.ent[base + rank] = (uint16_t)f;
-                if (rank == 0) cnt[e] = base + __popcll(same);
-            }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (e[i] < 0) continue;
+        u32x4 before = *(const LdsWords*)sc.of(e[i]);
+        const int c = i * kWaves + wave;               // chunks from c on do not count
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int bytes = min(max(c - 4 * j, 0), 4);
+            before[j] = bytes == 4 ? before[j] : before[j] & ((1u << (8 * bytes)) - 1);
         }
-        __syncthreads();
+        l.ent[start[e[i]] + entries(before) + rank[i]] = (uint16_t)((i * kWaves + wave) * kWave + lane);
     }
+    __syncthreads();
 }
 
 // The same for at most 64 entries, by one wave on its own (experts in the order of their
@@ -206,7 +236,8 @@ __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds, u
 // One of the two products.  UP: the rows are those of W1 and W3, a wave has 16 of each, the
 // other factor is x (one part); else they are those of W2, 32 of a wave, times the P
 // parts of h.  NT: 16 entries per wave and pass times NT.  SK: elements of a stage.
-template <bool MX, bool UP, int P, int NT, int SK, int WAVES>
+// SPLIT: all waves have the same rows, each its own stretch of K, and their sums are added.
+template <bool MX, bool UP, int P, int NT, int SK, int WAVES, bool SPLIT>
 struct Stream {
     static constexpr int kThreads = WAVES * kWave;
     static constexpr int kStageK = SK;
@@ -219,12 +250,14 @@ struct Stream {
     static constexpr int kColChunks = kStageK / 8;              // 16-byte chunks of an entry's row
     static constexpr int kColsPer = kWave / kColChunks;
     static constexpr int kColLoads = 16 * NT / kColsPer;        // loads of one part of all entries
-    static constexpr int kLoadsB = (kColLoads + WAVES - 1) / WAVES;   // of a wave and part
+    static constexpr int kLoadsB = SPLIT ? kColLoads : (kColLoads + WAVES - 1) / WAVES;   // of a wave and part
     static constexpr int kPart = 16 * NT * kColChunks * 16;
     static constexpr int kW = WAVES * 32 * kRowBytes;
-    static constexpr int kStageBytes = kW + P * kPart;
-    static constexpr int kRows = WAVES * (UP ? 16 : 32);        // output rows of an item
+    static constexpr int kStageBytes = kW + (SPLIT ? WAVES : 1) * P * kPart;
+    static constexpr int kRows = (SPLIT ? 1 : WAVES) * (UP ? 16 : 32);    // output rows of an item
     static constexpr int kLoads = kLoadsW + P * kLoadsB;        // of a wave for a stage
+    // waves on a SIMD, as far as the LDS lets the compiler count on them
+    static constexpr int kPerSimd = kLdsPerCu / (kGroup * kStageBytes) * WAVES >= 8 ? 2 : 1;
     static_assert(kRowBytes == 128 || kRowBytes == 64, "whole or half cache lines");
 };
 
@@ -237,24 +270,24 @@ struct Cursor {
     uint32_t col[LB];
 };
 
-template <bool MX, bool UP, int P, int NT, int SK, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uint32_t* lists,
-                                                               uint16_t* h, int64_t h_part,
-                                                               float* y, int h_parts) {
-    using S = Stream<MX, UP, P, NT, SK, WAVES>;
+template <bool MX, bool UP, int P, int NT, int SK, int WAVES, bool SPLIT>
+__global__ __launch_bounds__(WAVES * 64, (Stream<MX, UP, P, NT, SK, WAVES, SPLIT>::kPerSimd))
+void stream_kernel(DecodeArgs a, uint32_t* lists, uint16_t* h, int64_t h_part, float* y, int h_parts) {
+    using S = Stream<MX, UP, P, NT, SK, WAVES, SPLIT>;
     constexpr int kThreads = S::kThreads;
     extern __shared__ __align__(16) uint32_t list_block[];
     __shared__ __align__(16) uint8_t lds0[S::kStageBytes], lds1[S::kStageBytes];
     __shared__ __align__(16) uint8_t lds2[S::kStageBytes], lds3[S::kStageBytes];
+    __shared__ f32x4 sums[SPLIT ? (WAVES - 1) * 2 * NT * kWave : 1];     // of all waves but the first
     const int N = (int)(a.T * a.K);
     const Lists l((uint16_t*)list_block, N);
     if constexpr (UP) {
         // the scratch of the lists is in the stages' space, which is not in use yet
-        static_assert(sizeof(int[1024]) <= S::kStageBytes, "scratch");
-        int(&cnt)[1024] = *reinterpret_cast<int(*)[1024]>(lds0);
-        int(&sum)[WAVES][2] = *reinterpret_cast<int(*)[WAVES][2]>(lds1);
+        constexpr int kCounts = ListScratch::kExperts * ListScratch::kChunks;
+        static_assert(kCounts + 2048 <= S::kStageBytes, "scratch");
+        const ListScratch scratch{(Lds*)lds0, (Lds*)lds1, (Lds*)lds2, (Lds*)lds3, (int(*)[2])(lds1 + kCounts)};
         if (N > kWave) {
-            build_lists<kThreads>(a.idx, N, a.E, 16 * NT, l, cnt, sum);
+            build_lists<kThreads>(a.idx, N, a.E, 16 * NT, l, scratch, (uint16_t*)(lds0 + kCounts));
         } else {
             if (threadIdx.x < kWave) build_short_lists(a.idx, N, a.E, 16 * NT, l);
             __syncthreads();
@@ -271,7 +304,10 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
     const int blocks = (int)((M + S::kRows - 1) / S::kRows);
     const int items = __builtin_amdgcn_readfirstlane((int)*l.n) * blocks;
     const int chunks = (int)(MX ? K / 32 : K / 8), col_chunks = (int)(K / 8);
-    const int groups = (int)((K + S::kStageK * kGroup - 1) / (S::kStageK * kGroup));
+    constexpr int kGroupK = S::kStageK * kGroup * (SPLIT ? WAVES : 1);
+    const int groups = (int)((K + kGroupK - 1) / kGroupK);      // of a wave
+    const int row_wave = SPLIT ? 0 : wave;                      // by rows, and by stretches of K
+    const int k_wave = SPLIT ? wave : 0;
     const int64_t rb = MX ? K / 2 : K * 2, wrows = UP ? 2 * M : M;
 
     auto item_rows = [&](int item, int& slot) {
@@ -288,7 +324,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
         c.rows = (int)(M - r0 < S::kRows ? M - r0 : S::kRows);
 #pragma unroll
         for (int i = 0; i < S::kLoadsB; ++i) {
-            const int col = (wave * S::kLoadsB + i) % S::kColLoads * S::kColsPer + lane / S::kColChunks;
+            const int col = (row_wave * S::kLoadsB + i) % S::kColLoads * S::kColsPer + lane / S::kColChunks;
             const int f = l.ent[first + (col < n ? col : 0)];
             c.col[i] = (uint32_t)((UP ? f / a.K : f) * K * 2) | outside_if(col >= n);
         }
@@ -297,13 +333,14 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
     // that read one chunk of 8 rows meet different banks.
     const void* weights = UP ? a.w13 : a.w2;
     auto load_stage = [&](uint8_t* lds, const Cursor<S::kLoadsB>& c, int s) {
+        s += k_wave * groups * kGroup;
         const auto first = rows_of(weights, c.row, c.rows, rb);
         const auto second = UP ? rows_of(weights, c.row + M, c.rows, rb) : first;
 #pragma unroll
         for (int i = 0; i < S::kLoadsW; ++i) {
             const int r = i * S::kRowsPer + lane / S::kRowChunks;     // of the wave's 32
             const int at = s * S::kRowChunks + ((lane % S::kRowChunks) ^ (S::kLine ? r % 8 : r / 2 % 4));
-            const int row = UP ? wave * 16 + r % 16 : wave * 32 + r;
+            const int row = UP ? row_wave * 16 + r % 16 : row_wave * 32 + r;
             to_lds<S::kLine>(UP && i * S::kRowsPer >= 16 ? second : first, lds + (wave * 32 + i * S::kRowsPer) * S::kRowBytes,
                    ((uint32_t)row * (uint32_t)rb + (uint32_t)at * 16) | outside_if(at >= chunks));
         }
@@ -312,10 +349,10 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
             const auto src = UP ? rows_of(a.x, 0, a.T, K * 2) : rows_of(h + p * h_part, 0, N, K * 2);
 #pragma unroll
             for (int i = 0; i < S::kLoadsB; ++i) {
-                const int load = (wave * S::kLoadsB + i) % S::kColLoads;
+                const int load = (row_wave * S::kLoadsB + i) % S::kColLoads;
                 const int col = load * S::kColsPer + lane / S::kColChunks;
                 const int at = s * S::kColChunks + ((lane % S::kColChunks) ^ (col % 8));
-                to_lds<false>(src, lds + S::kW + p * S::kPart + load * 1024,
+                to_lds<false>(src, lds + S::kW + (k_wave * P + p) * S::kPart + load * 1024,
                        (c.col[i] + (uint32_t)at * 16) | outside_if(at >= col_chunks));
             }
         }
@@ -333,13 +370,13 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
     int next_move[2] = {}, next_valid = 0;     // bytes to drop in front, bytes of the row behind them
     auto load_scales = [&](const Cursor<S::kLoadsB>& c, int group) {
         if constexpr (MX) {
-            const int b0 = group * S::kWords * 4 + g * 16;
+            const int b0 = (k_wave * groups + group) * S::kWords * 4 + g * 16;
             const int end = c.rows * nblk - 16;         // (c.rows is a multiple of 32)
             next_valid = nblk - b0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const auto src = rows_of(UP ? a.s13 : a.s2, UP && i ? c.row + M : c.row, c.rows, nblk);
-                const int row = UP ? wave * 16 + r : wave * 32 + i * 16 + r;
+                const int row = UP ? row_wave * 16 + r : row_wave * 32 + i * 16 + r;
                 const int at = row * nblk + b0;
                 next_move[i] = max(at - end, 0);
                 next_scale[i] = __builtin_amdgcn_raw_buffer_load_b128(src, min(at, end), 0, 0);
@@ -374,7 +411,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
     bool nan[2] = {};     // whether the lane has met the NaN scale in its row
     auto use_stage = [&](const uint8_t* lds, int stage) {
         const uint8_t* wa = lds + wave * 32 * S::kRowBytes + r * S::kRowBytes;
-        const uint8_t* wb = lds + S::kW + r * S::kColChunks * 16;
+        const uint8_t* wb = lds + S::kW + k_wave * P * S::kPart + r * S::kColChunks * 16;
         auto other = [&](int p, int c, int chunk) {
             return as_bf16(ld16(wb + p * S::kPart + c * 16 * S::kColChunks * 16 + ((chunk ^ (r % 8)) * 16)));
         };
@@ -446,12 +483,34 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
                         for (int c = 0; c < NT; ++c) acc[i][c][q] = __builtin_nanf("");
             }
         }
+        if constexpr (SPLIT) {
+            // (the next item's sums come behind barriers that the first wave passes as well)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+                    if (wave > 0) sums[((wave - 1) * 2 * NT + i * NT + c) * kWave + lane] = acc[i][c];
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0xc07f);     // LDS writes are done
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if (wave > 0) {
+                clear();
+                return;
+            }
+#pragma unroll
+            for (int k = 0; k < WAVES - 1; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int c = 0; c < NT; ++c) acc[i][c] += sums[(k * 2 * NT + i * NT + c) * kWave + lane];
+        }
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
             const int col = c * 16 + r;
             const int f = l.ent[first + (col < n ? col : 0)];
             if constexpr (UP) {
-                const int64_t i = r0 + wave * 16 + 4 * g;
+                const int64_t i = r0 + row_wave * 16 + 4 * g;
                 float v[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[q] = silu_of(acc[0][c][q]) * acc[1][c][q];
@@ -466,7 +525,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void stream_kernel(DecodeArgs a, uin
             } else {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int64_t row = r0 + wave * 32 + i * 16 + 4 * g;
+                    const int64_t row = r0 + row_wave * 32 + i * 16 + 4 * g;
                     if (col < n && row < M) *(f32x4*)(y + f * a.H + row) = acc[i][c];
                 }
             }
@@ -576,18 +635,24 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(DecodeArgs a, const 
 }
 
 // Workgroups: as many as fit the card at once (LDS decides), or one per item.
-template <bool MX, bool UP, int P, int NT, int SK, int WAVES>
+template <bool MX, bool UP, int P, int NT, int SK, int WAVES, bool SPLIT>
 hipError_t launch(const DecodeArgs& a, uint32_t* lists, uint16_t* h, int64_t h_part, float* y, int parts,
                   hipStream_t s) {
-    using S = Stream<MX, UP, P, NT, SK, WAVES>;
+    using S = Stream<MX, UP, P, NT, SK, WAVES, SPLIT>;
     const int64_t N = a.T * a.K, M = UP ? a.I : a.H;
     const int64_t most = N * ((M + S::kRows - 1) / S::kRows);
     const size_t lists_lds = (size_t)list_words(N) * 4;
-    const int per_cu = (int)(kLdsPerCu / (kGroup * S::kStageBytes + lists_lds));
+    const int per_cu = (int)(kLdsPerCu / (kGroup * S::kStageBytes + (SPLIT ? (WAVES - 1) * NT * 2048 : 16) + lists_lds));
     const int64_t fit = (int64_t)256 * (per_cu < 1 ? 1 : per_cu);
-    stream_kernel<MX, UP, P, NT, SK, WAVES><<<dim3((unsigned)(most < fit ? most : fit)), S::kThreads, lists_lds, s>>>(
-        a, lists, h, h_part, y, parts);
+    stream_kernel<MX, UP, P, NT, SK, WAVES, SPLIT>
+        <<<dim3((unsigned)(most < fit ? most : fit)), S::kThreads, lists_lds, s>>>(a, lists, h, h_part, y, parts);
     return hipGetLastError();
+}
+
+// Slots that the entries of the experts in use fill, about.
+int64_t slots_of(const DecodeArgs& a, int width) {
+    const int64_t N = a.T * a.K, used = N < a.E ? N : a.E, full = (2 * N / width + used) / 2;
+    return full > used ? full : used;
 }
 
 template <bool MX, bool UP, int P, int NT, int SK>
@@ -596,13 +661,15 @@ hipError_t launch_waves(const DecodeArgs& a, uint32_t* lists, uint16_t* h, int64
     const int64_t N = a.T * a.K, used = N < a.E ? N : a.E, M = UP ? a.I : a.H;
     // 4 waves share the entries' rows; 2 where 4 would leave CUs without work
     if (used * ((M + (UP ? 63 : 127)) / (UP ? 64 : 128)) >= 512)
-        return launch<MX, UP, P, NT, SK, 4>(a, lists, h, h_part, y, parts, s);
-    return launch<MX, UP, P, NT, SK, 2>(a, lists, h, h_part, y, parts, s);
+        return launch<MX, UP, P, NT, SK, 4, false>(a, lists, h, h_part, y, parts, s);
+    return launch<MX, UP, P, NT, SK, 2, false>(a, lists, h, h_part, y, parts, s);
 }
 
 template <bool MX, bool UP, int P, int NT>
 hipError_t launch_stage(const DecodeArgs& a, uint32_t* lists, uint16_t* h, int64_t h_part, float* y,
-                        int parts, hipStream_t s) {
+                        int parts, bool split, hipStream_t s) {
+    if constexpr (UP && NT == 1)
+        if (split) return launch<MX, UP, P, NT, MX ? 128 : 64, 4, true>(a, lists, h, h_part, y, parts, s);
     if constexpr (!MX) {
         return launch_waves<MX, UP, P, NT, 64>(a, lists, h, h_part, y, parts, s);
     } else {
@@ -616,14 +683,14 @@ hipError_t launch_stage(const DecodeArgs& a, uint32_t* lists, uint16_t* h, int64
 }
 
 template <bool MX, int P, int NT>
-hipError_t launch_all(const DecodeArgs& a, hipStream_t s) {
+hipError_t launch_all(const DecodeArgs& a, bool split, hipStream_t s) {
     const int64_t N = a.T * a.K;
     uint32_t* lists = (uint32_t*)a.ws;
     float* y = (float*)((char*)a.ws + kListBytes);
     uint16_t* h = (uint16_t*)(y + N * a.H);
     const int64_t h_part = N * a.I;
-    hipError_t st = launch_stage<MX, true, 1, NT>(a, lists, h, h_part, y, P, s);
-    if (st == hipSuccess) st = launch_stage<MX, false, P, NT>(a, lists, h, h_part, y, P, s);
+    hipError_t st = launch_stage<MX, true, 1, NT>(a, lists, h, h_part, y, P, split, s);
+    if (st == hipSuccess) st = launch_stage<MX, false, P, NT>(a, lists, h, h_part, y, P, false, s);
     if (st != hipSuccess) return st;
     const dim3 grid((unsigned)((a.H + 4 * kJoinThreads - 1) / (4 * kJoinThreads)), (unsigned)a.T);
     join_kernel<<<grid, kJoinThreads, 0, s>>>(a, y);
@@ -632,10 +699,15 @@ hipError_t launch_all(const DecodeArgs& a, hipStream_t s) {
 
 template <bool MX>
 hipError_t launch_type(const DecodeArgs& a, hipStream_t s) {
+    // The first product's K is split over the waves where that still leaves a CU no more than
+    // two items, in us without and with: bf16 64 items 26.3, 18.5, 256 35.0, 28.4, 512 40.6,
+    // 39.1, 1088 40.2, 56.2; MXFP4 36 items 47.0, 26.3, 128 23.5, 17.9, 320 33.5, 25.3, 512
+    // 26.4, 26.1, 768 22.4, 25.7, 1024 32.6, 41.2.
+    const bool split = slots_of(a, 16) * ((a.I + 15) / 16) <= 512;
     // entries of an expert on average: 16 of them are worked on at once, or 32
-    const bool wide = a.T * a.K > 8 * (int64_t)a.E;
-    if (a.out_f32) return wide ? launch_all<MX, 3, 2>(a, s) : launch_all<MX, 3, 1>(a, s);
-    return wide ? launch_all<MX, 2, 2>(a, s) : launch_all<MX, 2, 1>(a, s);
+    const bool wide = !split && a.T * a.K > 8 * (int64_t)a.E;
+    if (a.out_f32) return wide ? launch_all<MX, 3, 2>(a, split, s) : launch_all<MX, 3, 1>(a, split, s);
+    return wide ? launch_all<MX, 2, 2>(a, split, s) : launch_all<MX, 2, 1>(a, split, s);
 }
 
 }  // namespace

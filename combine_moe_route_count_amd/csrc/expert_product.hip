@@ -21,12 +21,14 @@
 // chunk g.  The body of a stage is one block without a branch: with one the compiler moves
 // the matrix instructions behind it, away from the loads they were to cover.
 //
-// Scales are loaded for four stages at once, one 16-byte load per row where rows start at whole
-// words: loads of single words kept the address unit busier than the matrix cores.
+// Scales are loaded for eight stages at once, 16 bytes by each of two lanes where rows start at
+// whole words: loads of single words kept the address unit busier than the matrix cores.
 //
-// Measured on rows of random codes: 2.9e15 operations a second (32768 rows x 4096 x 7168 over
-// 64 experts, SwiGLU), 3.6e15 (8192 x 8192 x 8192), where the matrix instruction alone runs at
-// 6.3e15; 5.6 TB/s of weights where experts have two rows each (128 experts, 4096 x 4096).
+// Measured on random codes: 2.9 to 3.1e15 operations a second (32768 rows x 4096 x 7168 over
+// 64 experts, SwiGLU), 3.6 to 3.9e15 (8192 x 8192 x 8192), where the matrix instruction alone runs at
+// 6.3e15; all-zero codes take a quarter less time, so it is power that bounds it, and rows of
+// zeros in a tile cost little.  5.9 TB/s of weights where experts have two rows each (128
+// experts, 4096 x 4096).
 //
 // Rows behind a segment, weight rows behind N and chunks behind H are loaded as zeros
 // by the range check of the buffer descriptors (their scales too, so a NaN scale of a
@@ -258,15 +260,42 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
         }
         return v;
     };
+    // Pairs of groups whose weight scales are loaded at once: a cache line of them, where weight
+    // rows are read once, lest the line leave the L2 before its next quarter is wanted (weights
+    // of 128 experts, 4096 x 4096: 1222 -> 1040 MB from memory, 176 -> 166 us for 256 rows).
+    // 128 rows have no registers left for that: 288 -> 295 us (8192 rows of 64 experts).
+    constexpr int kAhead = BM <= 64 ? 4 : 1;
     u32x4 qw[NT], qa[MT], next_qw[NT], next_qa[MT];
-    auto load_scales = [&](int group, auto load) {
+    u32x4 ready_qw[kAhead][NT], flying_qw[kAhead][NT];
+    auto load_rest = [&](int group) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int tr = wn * NT + i;
-            next_qw[i] = load(SWIGLU && (i & 1) ? rsu : rsw, weight_row(tr * 32) + r, group);
+            next_qw[i] = scale_rest(SWIGLU && (i & 1) ? rsu : rsw, weight_row(tr * 32) + r, group);
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i) next_qa[i] = load(rsa, (wm * MT + i) * 32 + r, group);
+        for (int i = 0; i < MT; ++i) next_qa[i] = scale_rest(rsa, (wm * MT + i) * 32 + r, group);
+    };
+    auto load_w_pairs = [&](int group) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const int tr = wn * NT + i;
+                flying_qw[k][i] = scale_pair(SWIGLU && (i & 1) ? rsu : rsw, weight_row(tr * 32) + r, group + 2 * k);
+            }
+    };
+    auto load_a_pair = [&](int group) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) next_qa[i] = scale_pair(rsa, (wm * MT + i) * 32 + r, group);
+    };
+    auto next_pair = [&] {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            next_qw[i] = ready_qw[0][i];
+#pragma unroll
+            for (int k = 1; k < kAhead; ++k) ready_qw[k - 1][i] = ready_qw[k][i];
+        }
     };
     // Both halves of a wave get the lower half's group (HALF 0) or the upper half's.
     auto of_half = [](u32x4 v, auto half) {
@@ -379,7 +408,10 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
     MOE_MX_STAGE(lds3, lds0, 3)
 
     const int pairs = WORDS ? nblk / (2 * kGroupChunks) : 0;
-    if constexpr (WORDS) load_scales(0, scale_pair);
+    if constexpr (WORDS) {
+        load_w_pairs(0);
+        load_a_pair(0);
+    }
     load_stage(lds0, 0);
     load_stage(lds1, 1);      // past the last stage: zeros
     load_stage(lds2, 2);
@@ -389,17 +421,27 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
     int s = 0;
     sync(std::integral_constant<int, 3 * kLoads>{});
     read_frags(0, lds0);
-    for (int p = 1; p <= pairs; ++p) {
-        take_half(std::integral_constant<int, 0>{});
-        MOE_MX_GROUP();
-        take_half(std::integral_constant<int, 1>{});
-        load_scales(2 * p, scale_pair);     // behind the last pair: not used
-        MOE_MX_GROUP();
+    for (int p = 0; p < pairs;) {      // what is loaded behind the last pair is not used
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) ready_qw[k][i] = flying_qw[k][i];
+        load_w_pairs(2 * (p + kAhead));
+        const int end = min(p + kAhead, pairs);
+#pragma unroll 1
+        for (; p < end; ++p) {
+            next_pair();
+            take_half(std::integral_constant<int, 0>{});
+            MOE_MX_GROUP();
+            take_half(std::integral_constant<int, 1>{});
+            load_a_pair(2 * p + 2);
+            MOE_MX_GROUP();
+        }
     }
-    if (s < stages) load_scales(2 * pairs, scale_rest);
+    if (s < stages) load_rest(2 * pairs);
     while (s + kGroup <= stages) {
         take_rest(s / kGroup);
-        load_scales(s / kGroup + 1, scale_rest);
+        load_rest(s / kGroup + 1);
         MOE_MX_GROUP();
     }
     take_rest(s / kGroup);
@@ -470,7 +512,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
 // height: 4096 rows of 64 experts (4096 x 7168) 241 -> 232 us, 8192 295 -> 285.  (At 256 rows
 // it did not pay: 650 -> 659 us for 32768 rows.)
 template <int BM, bool SWIGLU, bool WORDS>
-__global__ __launch_bounds__(kThreads, 1) void product_kernel(ProductArgs a, int col_tiles,
+__global__ __launch_bounds__(kThreads, (BM <= 64 ? 2 : 1)) void product_kernel(ProductArgs a, int col_tiles,
                                                               int64_t base) {
     constexpr int kLds = (BM + kBN) * kStageBytes;
     __shared__ __align__(16) uint8_t lds0[kLds], lds1[kLds], lds2[kLds], lds3[kLds];

@@ -23,13 +23,13 @@
 //
 // h between the products is held in as many bf16 parts as the result can show: 2 (16 bits
 // of significand) for a bf16 result, 3 (24 bits) for an f32 one.  Each part costs one
-// matrix instruction per weight fragment, which bf16 weights have to spare; with MXFP4
-// weights, which must be widened too, the second product is bound by its instructions.
+// matrix instruction per weight fragment, which bf16 weights have to spare.  MXFP4 weights
+// must be widened too and leave less room: where experts have few entries the parts are
+// columns of one instruction, and the columns of an entry are added at the end.
 //
 // Measured, bytes of the weights in use over the time: one token and bf16 weights of 8
 // experts, 1024 x 6144, 54 us, 5.6 TB/s; 32 tokens and MXFP4 weights of 111 experts, 1024 x
-// 7168, 251 us, 5.2 TB/s (first product 152, second 93, sum 4); bf16, 1024 x 4096, 481 us,
-// 5.8 TB/s.
+// 7168, 238 us, 5.5 TB/s; bf16, 1024 x 4096, 481 us, 5.8 TB/s.
 #include <type_traits>
 
 #include "train_device.hpp"
@@ -207,6 +207,34 @@ __device__ void build_short_lists(const int32_t* idx, int N, int E, int width, c
     }
 }
 
+// The lists of a product that takes fewer entries at a time, `width`, from those at hand.
+__device__ void write_lists(const Lists& l, int width, const Lists& out) {
+    const int lane = threadIdx.x % kWave, n = *l.n, used = l.first[n];
+    for (int i = threadIdx.x; i < used; i += blockDim.x) out.ent[i] = l.ent[i];
+    if (threadIdx.x >= kWave) return;
+    int base = 0;
+    for (int c = 0; c < n; c += kWave) {
+        const int s = c + lane;
+        const int first = s < n ? l.first[s] : 0, cnt = s < n ? l.first[s + 1] - first : 0;
+        const int mine = (cnt + width - 1) / width;
+        int upto = mine;
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2) {
+            const int o = __shfl_up(upto, d);
+            if (lane >= d) upto += o;
+        }
+        for (int j = 0; j < mine; ++j) {
+            out.expert[base + upto - mine + j] = l.expert[s];
+            out.first[base + upto - mine + j] = (uint16_t)(first + j * width);
+        }
+        base += readlane(upto, kWave - 1);
+    }
+    if (lane == 0) {
+        *out.n = (uint16_t)base;
+        out.first[base] = (uint16_t)used;
+    }
+}
+
 __device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 // Two e2m1 codes (byte SEL of d) times 2^(scale's exponent), as bf16.
@@ -245,8 +273,13 @@ __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds, u
 // other factor is x (one part); else they are those of W2, 32 of a wave, times the P
 // parts of h.  NT: 16 entries per wave and pass times NT.  SK: elements of a stage.
 // SPLIT: all waves have the same rows, each its own stretch of K, and their sums are added.
-template <bool MX, bool UP, int P, int NT, int SK, int WAVES, bool SPLIT>
+// PACK: the parts of h are columns of their own, 16 / P entries at a time, and the columns
+// of an entry are added at the end.
+template <bool MX, bool UP, int P, int NT, int SK, int WAVES, bool SPLIT, bool PACK>
 struct Stream {
+    static_assert(!PACK || (!UP && NT == 1 && !SPLIT), "parts as columns");
+    static constexpr int kWidth = PACK ? 16 / P : 16 * NT;      // entries at a time
+    static constexpr int kParts = PACK ? 1 : P;                 // of the stages in LDS
     static constexpr int kThreads = WAVES * kWave;
     static constexpr int kStageK = SK;
     static constexpr int kRowBytes = MX ? SK / 2 : SK * 2;      // of a weight row in a stage
@@ -261,9 +294,9 @@ struct Stream {
     static constexpr int kLoadsB = SPLIT ? kColLoads : (kColLoads + WAVES - 1) / WAVES;   // of a wave and part
     static constexpr int kPart = 16 * NT * kColChunks * 16;
     static constexpr int kW = WAVES * 32 * kRowBytes;
-    static constexpr int kStageBytes = kW + (SPLIT ? WAVES : 1) * P * kPart;
+    static constexpr int kStageBytes = kW + (SPLIT ? WAVES : 1) * kParts * kPart;
     static constexpr int kRows = (SPLIT ? 1 : WAVES) * (UP ? 16 : 32);    // output rows of an item
-    static constexpr int kLoads = kLoadsW + P * kLoadsB;        // of a wave for a stage
+    static constexpr int kLoads = kLoadsW + kParts * kLoadsB;        // of a wave for a stage
     // waves on a SIMD, as far as the LDS lets the compiler count on them
     static constexpr int kPerSimd = kLdsPerCu / (kGroup * kStageBytes) * WAVES >= 8 ? 2 : 1;
     static_assert(kRowBytes == 128 || kRowBytes == 64, "whole or half cache lines");
@@ -278,11 +311,12 @@ struct Cursor {
     uint32_t col[LB];
 };
 
-template <bool MX, bool UP, int P, int NT, int SK, int WAVES, bool SPLIT>
-__global__ __launch_bounds__(WAVES * 64, (Stream<MX, UP, P, NT, SK, WAVES, SPLIT>::kPerSimd))
-void stream_kernel(DecodeArgs a, uint32_t* lists, uint16_t* h, int64_t h_part, float* y, int h_parts) {
-    using S = Stream<MX, UP, P, NT, SK, WAVES, SPLIT>;
-    constexpr int kThreads = S::kThreads;
+// down_width: entries that the second product takes at a time.
+template <bool MX, bool UP, int P, int NT, int SK, int WAVES, bool SPLIT, bool PACK>
+__global__ __launch_bounds__(WAVES * 64, (Stream<MX, UP, P, NT, SK, WAVES, SPLIT, PACK>::kPerSimd))
+void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, int64_t h_part, float* y, int h_parts) {
+    using S = Stream<MX, UP, P, NT, SK, WAVES, SPLIT, PACK>;
+    constexpr int kThreads = S::kThreads, kParts = S::kParts;
     extern __shared__ __align__(16) uint32_t list_block[];
     __shared__ __align__(16) uint8_t lds0[S::kStageBytes], lds1[S::kStageBytes];
     __shared__ __align__(16) uint8_t lds2[S::kStageBytes], lds3[S::kStageBytes];
@@ -300,8 +334,10 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, uint16_t* h, int64_t h_part, f
             if (threadIdx.x < kWave) build_short_lists(a.idx, N, a.E, 16 * NT, l);
             __syncthreads();
         }
-        if (blockIdx.x == 0)
-            for (int i = threadIdx.x; i < list_words(N); i += kThreads) lists[i] = list_block[i];
+        if (blockIdx.x == gridDim.x - 1) {        // has nothing else to do
+            write_lists(l, down_width, Lists((uint16_t*)lists, N));
+            return;
+        }
     } else {
         for (int i = threadIdx.x; i < list_words(N); i += kThreads) list_block[i] = lists[i];
         __syncthreads();
@@ -311,6 +347,7 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, uint16_t* h, int64_t h_part, f
     const int64_t K = UP ? a.H : a.I, M = UP ? a.I : a.H;     // sum length, output rows of an expert
     const int blocks = (int)((M + S::kRows - 1) / S::kRows);
     const int items = __builtin_amdgcn_readfirstlane((int)*l.n) * blocks;
+    const int workers = (int)gridDim.x - (UP ? 1 : 0);
     const int chunks = (int)(MX ? K / 32 : K / 8), col_chunks = (int)(K / 8);
     constexpr int kGroupK = S::kStageK * kGroup * (SPLIT ? WAVES : 1);
     const int groups = (int)((K + kGroupK - 1) / kGroupK);      // of a wave
@@ -333,8 +370,12 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, uint16_t* h, int64_t h_part, f
 #pragma unroll
         for (int i = 0; i < S::kLoadsB; ++i) {
             const int col = (row_wave * S::kLoadsB + i) % S::kColLoads * S::kColsPer + lane / S::kColChunks;
-            const int f = l.ent[first + (col < n ? col : 0)];
-            c.col[i] = (uint32_t)((UP ? f / a.K : f) * K * 2) | outside_if(col >= n);
+            // (of PACK, column col is part col / width of entry col % width)
+            const int part = PACK ? col / S::kWidth : 0, of = PACK ? col % S::kWidth : col;
+            const bool none = of >= n || part >= P;
+            const int f = l.ent[first + (none ? 0 : of)];
+            const int64_t row = (UP ? f / a.K : f) + (int64_t)(none ? 0 : part) * N;
+            c.col[i] = (uint32_t)(row * K * 2) | outside_if(none);
         }
     };
     // Stage s of an item into LDS.  A row's chunks stand at chunk ^ row bits, so that 8 lanes
@@ -353,14 +394,15 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, uint16_t* h, int64_t h_part, f
                    ((uint32_t)row * (uint32_t)rb + (uint32_t)at * 16) | outside_if(at >= chunks));
         }
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const auto src = UP ? rows_of(a.x, 0, a.T, K * 2) : rows_of(h + p * h_part, 0, N, K * 2);
+        for (int p = 0; p < kParts; ++p) {
+            const auto src = UP ? rows_of(a.x, 0, a.T, K * 2)
+                                : rows_of(h + p * h_part, 0, PACK ? (int64_t)N * P : N, K * 2);
 #pragma unroll
             for (int i = 0; i < S::kLoadsB; ++i) {
                 const int load = (row_wave * S::kLoadsB + i) % S::kColLoads;
                 const int col = load * S::kColsPer + lane / S::kColChunks;
                 const int at = s * S::kColChunks + ((lane % S::kColChunks) ^ (col % 8));
-                to_lds<false>(src, lds + S::kW + (k_wave * P + p) * S::kPart + load * 1024,
+                to_lds<false>(src, lds + S::kW + (k_wave * kParts + p) * S::kPart + load * 1024,
                        (c.col[i] + (uint32_t)at * 16) | outside_if(at >= col_chunks));
             }
         }
@@ -419,7 +461,7 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, uint16_t* h, int64_t h_part, f
     bool nan[2] = {};     // whether the lane has met the NaN scale in its row
     auto use_stage = [&](const uint8_t* lds, int stage) {
         const uint8_t* wa = lds + wave * 32 * S::kRowBytes + r * S::kRowBytes;
-        const uint8_t* wb = lds + S::kW + k_wave * P * S::kPart + r * S::kColChunks * 16;
+        const uint8_t* wb = lds + S::kW + k_wave * kParts * S::kPart + r * S::kColChunks * 16;
         auto other = [&](int p, int c, int chunk) {
             return as_bf16(ld16(wb + p * S::kPart + c * 16 * S::kColChunks * 16 + ((chunk ^ (r % 8)) * 16)));
         };
@@ -442,7 +484,7 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, uint16_t* h, int64_t h_part, f
 #pragma unroll
                     for (int i = 0; i < 2; ++i) w[i] = as_bf16(widen8(codes[i][q], f[i]));
 #pragma unroll
-                    for (int p = 0; p < P; ++p)
+                    for (int p = 0; p < kParts; ++p)
 #pragma unroll
                         for (int c = 0; c < NT; ++c) {
                             const bf16x8 b = other(p, c, part * 16 + 4 * g + q);
@@ -460,7 +502,7 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, uint16_t* h, int64_t h_part, f
                 for (int i = 0; i < 2; ++i)
                     w[i] = as_bf16(ld16(wa + i * 16 * S::kRowBytes + (((4 * q + g) ^ (r % 8)) * 16)));
 #pragma unroll
-                for (int p = 0; p < P; ++p)
+                for (int p = 0; p < kParts; ++p)
 #pragma unroll
                     for (int c = 0; c < NT; ++c) {
                         const bf16x8 b = other(p, c, 4 * q + g);
@@ -512,6 +554,16 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, uint16_t* h, int64_t h_part, f
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int c = 0; c < NT; ++c) acc[i][c] += sums[(k * 2 * NT + i * NT + c) * kWave + lane];
+        }
+        if constexpr (PACK) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const f32x4 own = acc[i][0];
+#pragma unroll
+                for (int p = 1; p < P; ++p)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[i][0][q] += __shfl_down(own[q], p * S::kWidth);
+            }
         }
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
@@ -569,7 +621,7 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, uint16_t* h, int64_t h_part, f
     for (int group = 0;;) {
         // where the stream goes after this group; behind the last item it loads zeros
         const bool last = group + 1 == groups;
-        const int next_item = last ? item + (int)gridDim.x : item;
+        const int next_item = last ? item + workers : item;
         const int next_group = last ? 0 : group + 1;
         const bool more = next_item < items;
         next = now;
@@ -642,18 +694,29 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(DecodeArgs a, const 
     else store_unit<false, false>(a.out, t * a.H + c, v);
 }
 
+struct Work {
+    uint32_t* lists;
+    int down_width;       // entries that the second product takes at a time
+    uint16_t* h;
+    int64_t h_part;       // elements of a part
+    float* y;
+    int parts;            // of h
+    bool split, pack;     // SPLIT of the first product, PACK of the second
+};
+
 // Workgroups: as many as fit the card at once (LDS decides), or one per item.
-template <bool MX, bool UP, int P, int NT, int SK, int WAVES, bool SPLIT>
-hipError_t launch(const DecodeArgs& a, uint32_t* lists, uint16_t* h, int64_t h_part, float* y, int parts,
-                  hipStream_t s) {
-    using S = Stream<MX, UP, P, NT, SK, WAVES, SPLIT>;
+template <bool MX, bool UP, int P, int NT, int SK, int WAVES, bool SPLIT, bool PACK>
+hipError_t launch(const DecodeArgs& a, const Work& w, hipStream_t s) {
+    using S = Stream<MX, UP, P, NT, SK, WAVES, SPLIT, PACK>;
     const int64_t N = a.T * a.K, M = UP ? a.I : a.H;
     const int64_t most = N * ((M + S::kRows - 1) / S::kRows);
     const size_t lists_lds = (size_t)list_words(N) * 4;
     const int per_cu = (int)(kLdsPerCu / (kGroup * S::kStageBytes + (SPLIT ? (WAVES - 1) * NT * 2048 : 16) + lists_lds));
     const int64_t fit = (int64_t)256 * (per_cu < 1 ? 1 : per_cu);
-    stream_kernel<MX, UP, P, NT, SK, WAVES, SPLIT>
-        <<<dim3((unsigned)(most < fit ? most : fit)), S::kThreads, lists_lds, s>>>(a, lists, h, h_part, y, parts);
+    // (one more writes the lists of the second product)
+    stream_kernel<MX, UP, P, NT, SK, WAVES, SPLIT, PACK>
+        <<<dim3((unsigned)((most < fit ? most : fit) + (UP ? 1 : 0))), S::kThreads, lists_lds, s>>>(
+            a, w.lists, w.down_width, w.h, w.h_part, w.y, w.parts);
     return hipGetLastError();
 }
 
@@ -663,45 +726,54 @@ int64_t slots_of(const DecodeArgs& a, int width) {
     return full > used ? full : used;
 }
 
-template <bool MX, bool UP, int P, int NT, int SK>
-hipError_t launch_waves(const DecodeArgs& a, uint32_t* lists, uint16_t* h, int64_t h_part, float* y,
-                        int parts, hipStream_t s) {
+template <bool MX, bool UP, int P, int NT, int SK, bool PACK = false>
+hipError_t launch_waves(const DecodeArgs& a, const Work& w, hipStream_t s) {
     const int64_t N = a.T * a.K, used = N < a.E ? N : a.E, M = UP ? a.I : a.H;
     // 4 waves share the entries' rows; 2 where 4 would leave CUs without work
     if (used * ((M + (UP ? 63 : 127)) / (UP ? 64 : 128)) >= 512)
-        return launch<MX, UP, P, NT, SK, 4, false>(a, lists, h, h_part, y, parts, s);
-    return launch<MX, UP, P, NT, SK, 2, false>(a, lists, h, h_part, y, parts, s);
+        return launch<MX, UP, P, NT, SK, 4, false, PACK>(a, w, s);
+    return launch<MX, UP, P, NT, SK, 2, false, PACK>(a, w, s);
 }
 
 template <bool MX, bool UP, int P, int NT>
-hipError_t launch_stage(const DecodeArgs& a, uint32_t* lists, uint16_t* h, int64_t h_part, float* y,
-                        int parts, bool split, hipStream_t s) {
+hipError_t launch_stage(const DecodeArgs& a, const Work& w, hipStream_t s) {
     if constexpr (UP && NT == 1)
-        if (split) return launch<MX, UP, P, NT, MX ? 128 : 64, 4, true>(a, lists, h, h_part, y, parts, s);
+        if (w.split) return launch<MX, UP, P, NT, MX ? 128 : 64, 4, true, false>(a, w, s);
+    if constexpr (!UP && NT == 1 && MX)
+        if (w.pack) return launch_waves<MX, UP, P, NT, 128, true>(a, w, s);
     if constexpr (!MX) {
-        return launch_waves<MX, UP, P, NT, 64>(a, lists, h, h_part, y, parts, s);
+        return launch_waves<MX, UP, P, NT, 64>(a, w, s);
     } else {
         // Whole cache lines of MXFP4 rows where a group of stages of 256 is not mostly zeros: 163 ->
         // 152 us (111 experts' W1 and W3 of 1024 x 7168).  Not with the parts of h: their stages
         // leave the CU one workgroup, 97 -> 114 us (W2 of 7168 x 1024).
         if constexpr (NT == 1 && P == 1)
-            if (a.H >= 768) return launch_waves<MX, UP, P, NT, 256>(a, lists, h, h_part, y, parts, s);
-        return launch_waves<MX, UP, P, NT, 128>(a, lists, h, h_part, y, parts, s);
+            if (a.H >= 768) return launch_waves<MX, UP, P, NT, 256>(a, w, s);
+        return launch_waves<MX, UP, P, NT, 128>(a, w, s);
     }
 }
 
 template <bool MX, int P, int NT>
 hipError_t launch_all(const DecodeArgs& a, bool split, hipStream_t s) {
     const int64_t N = a.T * a.K;
-    uint32_t* lists = (uint32_t*)a.ws;
-    float* y = (float*)((char*)a.ws + kListBytes);
-    uint16_t* h = (uint16_t*)(y + N * a.H);
-    const int64_t h_part = N * a.I;
-    hipError_t st = launch_stage<MX, true, 1, NT>(a, lists, h, h_part, y, P, split, s);
-    if (st == hipSuccess) st = launch_stage<MX, false, P, NT>(a, lists, h, h_part, y, P, false, s);
+    Work w{};
+    w.lists = (uint32_t*)a.ws;
+    w.y = (float*)((char*)a.ws + kListBytes);
+    w.h = (uint16_t*)(w.y + N * a.H);
+    w.h_part = N * a.I;
+    w.parts = P;
+    w.split = split;
+    // Parts as columns, in us without and with, by entries per expert: one token of 8 experts 49.1,
+    // 45.2 (4 experts a token, f32 result 49.4, 43.8); 2 240, 238 (f32 result 261, 240); 4 272, 270; 8
+    // 290, 298, where some experts have too many for one pass.  (The parts are read by one
+    // descriptor of less than 2^31 bytes.)
+    w.pack = MX && NT == 1 && N <= 4 * (int64_t)a.E && w.h_part * 2 * P < ((int64_t)1 << 31);
+    w.down_width = w.pack ? 16 / P : 16 * NT;
+    hipError_t st = launch_stage<MX, true, 1, NT>(a, w, s);
+    if (st == hipSuccess) st = launch_stage<MX, false, P, NT>(a, w, s);
     if (st != hipSuccess) return st;
     const dim3 grid((unsigned)((a.H + 4 * kJoinThreads - 1) / (4 * kJoinThreads)), (unsigned)a.T);
-    join_kernel<<<grid, kJoinThreads, 0, s>>>(a, y);
+    join_kernel<<<grid, kJoinThreads, 0, s>>>(a, w.y);
     return hipGetLastError();
 }
 

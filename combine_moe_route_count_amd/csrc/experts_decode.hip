@@ -29,7 +29,7 @@
 //
 // Measured, bytes of the weights in use over the time: one token and bf16 weights of 8
 // experts, 1024 x 6144, 54 us, 5.6 TB/s; 32 tokens and MXFP4 weights of 111 experts, 1024 x
-// 7168, 238 us, 5.5 TB/s; bf16, 1024 x 4096, 481 us, 5.8 TB/s.
+// 7168, 226 us, 5.8 TB/s; bf16, 1024 x 4096, 481 us, 5.8 TB/s.
 #include <type_traits>
 
 #include "train_device.hpp"
@@ -739,16 +739,19 @@ template <bool MX, bool UP, int P, int NT>
 hipError_t launch_stage(const DecodeArgs& a, const Work& w, hipStream_t s) {
     if constexpr (UP && NT == 1)
         if (w.split) return launch<MX, UP, P, NT, MX ? 128 : 64, 4, true, false>(a, w, s);
+    // Whole cache lines of MXFP4 rows (stages of 256) where a group of stages is not mostly zeros:
+    // 163 -> 152 us (111 experts' W1 and W3 of 1024 x 7168), 238 -> 226 both products (32 tokens).
+    // Not with the parts of h apart: their stages leave the CU one workgroup, 97 -> 114 us (W2).
+    constexpr int kLong = 768;
     if constexpr (!UP && NT == 1 && MX)
-        if (w.pack) return launch_waves<MX, UP, P, NT, 128, true>(a, w, s);
+        if (w.pack)
+            return a.I >= kLong ? launch_waves<MX, UP, P, NT, 256, true>(a, w, s)
+                                : launch_waves<MX, UP, P, NT, 128, true>(a, w, s);
     if constexpr (!MX) {
         return launch_waves<MX, UP, P, NT, 64>(a, w, s);
     } else {
-        // Whole cache lines of MXFP4 rows where a group of stages of 256 is not mostly zeros: 163 ->
-        // 152 us (111 experts' W1 and W3 of 1024 x 7168).  Not with the parts of h: their stages
-        // leave the CU one workgroup, 97 -> 114 us (W2 of 7168 x 1024).
         if constexpr (NT == 1 && P == 1)
-            if (a.H >= 768) return launch_waves<MX, UP, P, NT, 256>(a, w, s);
+            if (a.H >= kLong) return launch_waves<MX, UP, P, NT, 256>(a, w, s);
         return launch_waves<MX, UP, P, NT, 128>(a, w, s);
     }
 }

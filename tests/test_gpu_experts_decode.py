@@ -141,6 +141,16 @@ def test_scale_rows_at_any_byte(T, H, I, E, K, out):
     _check(y, _ref(x.double(), idx, w, w13[2], w2[2], 3 if out == F32 else 2), "scales")
 
 
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("T,K", [(5, 1), (11, 1), (20, 4), (33, 2)])
+def test_many_entries_of_one_expert_among_many(T, K, out):
+    """Few entries per expert on average, all of them on one: more than one pass over its weights."""
+    note(f"decode crowd T={T} K={K} {out}")
+    x, idx, w, w13, w2 = _inputs(T, 192, 96, 40, K, True, T, none=0.1, same=True)
+    y = _call(x, idx, w, w13, w2, out)
+    _check(y, _ref(x.double(), idx, w, w13[2], w2[2], 3 if out == F32 else 2), "crowd")
+
+
 @pytest.mark.parametrize("mx", [False, True])
 @pytest.mark.parametrize("T,E,K", [(1024, 1024, 1), (64, 5, 16), (1024, 1, 1)])
 def test_as_many_entries_as_are_allowed(T, E, K, mx):

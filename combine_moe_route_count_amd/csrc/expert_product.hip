@@ -145,8 +145,9 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs& a, int64_t b, int c
             e = e0 + c * kWave + owner;
         }
     }
-    if (tiles == 0) return t;      // counts that change under the call
     const int64_t local = item - (int64_t)before * col_tiles;
+    // counts that change under the call, or whose sum overflows because segments overlap
+    if (local < 0 || local >= (int64_t)tiles * col_tiles) return t;
     const int top = (int)(local / ((int64_t)kRowGroup * col_tiles)) * kRowGroup;
     const int rows = tiles - top < kRowGroup ? tiles - top : kRowGroup;
     const int in_group = (int)(local - (int64_t)top * col_tiles);

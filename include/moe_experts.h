@@ -55,8 +55,9 @@ int moe_mxfp4_dequantize(const void* codes, const void* scales, int64_t rows, in
  *   y[r,n] = sum_h a[r,h] * w[e,n,h]     for every row r of expert e's segment
  * or, with swiglu != 0, where a weight matrix is I gate rows and then I up rows, N = 2I:
  *   y[r,i] = silu(sum_h a[r,h] * w[e,i,h]) * sum_h a[r,h] * w[e,I+i,h]
- * E = 1 with one segment is an ordinary product.  Segments that overlap, which no
- * dispatch makes, leave the rows they share with the result of one of their experts.
+ * E = 1 with one segment is an ordinary product.  Segments must not overlap (no dispatch
+ * makes such): rows of those that do may be left as they were, or hold the result of
+ * either expert.
  *   a, a_scales  [rows,H/2] codes (16-byte aligned), [rows,H/32] scales, H % 32 == 0
  *   w, w_scales  [E,N,H/2] codes (16-byte aligned), [E,N,H/32] scales,
  *           N % 8 == 0 (N % 16 == 0 with swiglu), N <= 2^24

@@ -21,8 +21,8 @@
 // chunk g.  The body of a stage is one block without a branch: with one the compiler moves
 // the matrix instructions behind it, away from the loads they were to cover.
 //
-// Scales are loaded for eight stages at once, 16 bytes by each of two lanes where rows start at
-// whole words: loads of single words kept the address unit busier than the matrix cores.
+// Scales are loaded for eight stages at once, 16 bytes by each of two lanes, wherever rows start:
+// loads of single words kept the address unit busier than the matrix cores.
 //
 // Measured on random codes: 2.9 to 3.1e15 operations a second (32768 rows x 4096 x 7168 over
 // 64 experts, SwiGLU), 3.6 to 3.9e15 (8192 x 8192 x 8192), where the matrix instruction alone runs at
@@ -242,9 +242,9 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
     auto scale_pair = [&](__amdgpu_buffer_rsrc_t rs, int row, int group) -> u32x4 {
         return __builtin_amdgcn_raw_buffer_load_b128(rs, row * nblk + (group + g) * kGroupChunks, 0, 0);
     };
-    // What is left behind the pairs, or all where rows do not start at whole words: then the
-    // two bytes of each stage as they stand in memory, moved to their place when taken (a
-    // move here would wait for the load).  The last two of a row are read where fewer are left.
+    // What is left behind the pairs: a word for each stage, or, where rows do not start at whole
+    // words, its two bytes as they stand in memory, moved to their place when taken (a move
+    // here would wait for the load).  The last two of a row are read where fewer are left.
     auto scale_rest = [&](__amdgpu_buffer_rsrc_t rs, int row, int group) -> u32x4 {
         const uint32_t off = (uint32_t)row * (uint32_t)nblk;
         u32x4 v;
@@ -408,11 +408,9 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
     MOE_MX_STAGE(lds2, lds3, 2);    \
     MOE_MX_STAGE(lds3, lds0, 3)
 
-    const int pairs = WORDS ? nblk / (2 * kGroupChunks) : 0;
-    if constexpr (WORDS) {
-        load_w_pairs(0);
-        load_a_pair(0);
-    }
+    const int pairs = nblk / (2 * kGroupChunks);
+    load_w_pairs(0);
+    load_a_pair(0);
     load_stage(lds0, 0);
     load_stage(lds1, 1);      // past the last stage: zeros
     load_stage(lds2, 2);

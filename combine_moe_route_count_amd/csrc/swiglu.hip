@@ -15,8 +15,11 @@
 //
 // Both kernels are one pass over the rows, 8 elements of g and the same of u per lane (4
 // where the output is f32, so that a store is 16 bytes a lane and a wave's whole lines),
-// HBM bound.  A block of threads is `tx` lanes along a row times rows of it, so short
-// rows share a workgroup; rows outside every segment are neither read nor written.
+// HBM bound: 65536 x 2 x 2048 bf16 with the checkpoint 168 us, 6.4 TB/s; the gradient of the
+// same from the checkpoint, with h, 240 us, 5.6 TB/s; 16384 x 2 x 2048 f32 gradient 139 us.
+// With 8 f32 elements a lane (two stores to a lane, each half of every line) that one took
+// 157.  A workgroup is a power of two of lanes along a row times rows of it, so short rows
+// share one; rows outside every segment are neither read nor written.
 #include <type_traits>
 
 #include "train_device.hpp"
@@ -257,7 +260,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_grad_kernel(SwigluGradArgs a,
 }
 
 // Lanes along a row: the smallest power of two that covers its units, at least a block of
-// the checkpoint, within a workgroup.
+// the checkpoint, within a workgroup.  Lanes that leave fewer idle, but take turns on a row,
+// were slower: 13796 rows of 1280 bf16 48.4 -> 51.2 us, their gradient 35.2 -> 41.0.
 inline int log_width_of(int64_t I, bool out_f32) {
     int l = out_f32 ? 5 : 4;
     while (l < 8 && ((int64_t)elems_of(out_f32) << l) < I) ++l;

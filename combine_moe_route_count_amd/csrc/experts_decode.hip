@@ -311,8 +311,9 @@ struct Cursor {
     uint32_t col[LB];
 };
 
-// down_width: entries that the second product takes at a time.
-template <bool MX, bool UP, int P, int NT, int SK, int WAVES, bool SPLIT, bool PACK>
+// down_width: entries that the second product takes at a time.  ONCE: a stage of a weight row
+// is a cache line, which is not wanted again.
+template <bool MX, bool UP, int P, int NT, int SK, int WAVES, bool SPLIT, bool PACK, bool ONCE>
 __global__ __launch_bounds__(WAVES * 64, (Stream<MX, UP, P, NT, SK, WAVES, SPLIT, PACK>::kPerSimd))
 void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, int64_t h_part, float* y, int h_parts) {
     using S = Stream<MX, UP, P, NT, SK, WAVES, SPLIT, PACK>;
@@ -390,7 +391,7 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
             const int r = i * S::kRowsPer + lane / S::kRowChunks;     // of the wave's 32
             const int at = s * S::kRowChunks + ((lane % S::kRowChunks) ^ (S::kLine ? r % 8 : r / 2 % 4));
             const int row = UP ? row_wave * 16 + r % 16 : row_wave * 32 + r;
-            to_lds<S::kLine>(UP && i * S::kRowsPer >= 16 ? second : first, lds + (wave * 32 + i * S::kRowsPer) * S::kRowBytes,
+            to_lds<ONCE>(UP && i * S::kRowsPer >= 16 ? second : first, lds + (wave * 32 + i * S::kRowsPer) * S::kRowBytes,
                    ((uint32_t)row * (uint32_t)rb + (uint32_t)at * 16) | outside_if(at >= chunks));
         }
 #pragma unroll
@@ -421,7 +422,7 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
     auto load_scales = [&](const Cursor<S::kLoadsB>& c, int group) {
         if constexpr (MX) {
             const int b0 = (k_wave * groups + group) * S::kWords * 4 + g * 16;
-            const int end = c.rows * nblk - 16;         // (c.rows is a multiple of 32)
+            const int end = c.rows * nblk - 16;         // (c.rows is a multiple of 16)
             next_valid = nblk - b0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -714,10 +715,19 @@ hipError_t launch(const DecodeArgs& a, const Work& w, hipStream_t s) {
     const size_t lists_lds = (size_t)list_words(N) * 4;
     const int per_cu = (int)(kLdsPerCu / (kGroup * S::kStageBytes + (SPLIT ? (WAVES - 1) * NT * 2048 : 16) + lists_lds));
     const int64_t fit = (int64_t)256 * (per_cu < 1 ? 1 : per_cu);
+    // Weights go past the caches where rows are whole lines; a line that two stages share would be
+    // fetched twice: 640 us with, 707 without (32 tokens, bf16, 128 experts of 2816 x 2816), 889
+    // and 761 (2888 x 2888).
+    const int64_t rb = (UP ? a.H : a.I) * 2 / (MX ? 4 : 1);
+    const bool once = S::kLine && rb % 128 == 0 && (uintptr_t)(UP ? a.w13 : a.w2) % 128 == 0;
     // (one more writes the lists of the second product)
-    stream_kernel<MX, UP, P, NT, SK, WAVES, SPLIT, PACK>
-        <<<dim3((unsigned)((most < fit ? most : fit) + (UP ? 1 : 0))), S::kThreads, lists_lds, s>>>(
-            a, w.lists, w.down_width, w.h, w.h_part, w.y, w.parts);
+    const dim3 grid((unsigned)((most < fit ? most : fit) + (UP ? 1 : 0)));
+    if (S::kLine && once)
+        stream_kernel<MX, UP, P, NT, SK, WAVES, SPLIT, PACK, S::kLine>
+            <<<grid, S::kThreads, lists_lds, s>>>(a, w.lists, w.down_width, w.h, w.h_part, w.y, w.parts);
+    else
+        stream_kernel<MX, UP, P, NT, SK, WAVES, SPLIT, PACK, false>
+            <<<grid, S::kThreads, lists_lds, s>>>(a, w.lists, w.down_width, w.h, w.h_part, w.y, w.parts);
     return hipGetLastError();
 }
 

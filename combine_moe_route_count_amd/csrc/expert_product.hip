@@ -177,6 +177,21 @@ __device__ __forceinline__ float silu_of(float g) {
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
 }
 
+// Rows of scales from the word on in which the first begins, `skip` bytes before it.  The
+// range ends with the word that holds the last byte.
+struct Scales {
+    __amdgpu_buffer_rsrc_t rs;
+    int skip;
+};
+template <bool WORDS>
+__device__ __forceinline__ Scales scales_of(const uint8_t* base, int64_t row, int64_t rows, int64_t nblk) {
+    const uint8_t* p = base + row * nblk;
+    const int skip = WORDS ? 0 : (int)((uintptr_t)p & 3);
+    return Scales{__builtin_amdgcn_make_buffer_rsrc((void*)(p - skip), 0,
+                                                    (int)((uint32_t)(skip + rows * nblk + 3) & ~3u), kRsrcWord3),
+                  skip};
+}
+
 // Waves that share a tile's weight rows.
 constexpr int row_waves(int BM) { return BM >= 128 ? 2 : 1; }
 
@@ -207,9 +222,9 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
     const auto ra = rows_of(a.a, t.row0, t.rows, rb);
     const auto rw = rows_of(a.w, wrow, wrows, rb);
     const auto ru = SWIGLU ? rows_of(a.w, wrow + NO, wrows, rb) : rw;
-    const auto rsa = rows_of(a.a_scales, t.row0, t.rows, nblk);
-    const auto rsw = rows_of(a.w_scales, wrow, wrows, nblk);
-    const auto rsu = SWIGLU ? rows_of(a.w_scales, wrow + NO, wrows, nblk) : rsw;
+    const Scales rsa = scales_of<WORDS>(a.a_scales, t.row0, t.rows, nblk);
+    const Scales rsw = scales_of<WORDS>(a.w_scales, wrow, wrows, nblk);
+    const Scales rsu = SWIGLU ? scales_of<WORDS>(a.w_scales, wrow + NO, wrows, nblk) : rsw;
 
     // Weight row (within its half) of tile row r.
     auto weight_row = [](int r) { return SWIGLU ? (r >> 6) * 32 + (r & 31) : r; };
@@ -239,14 +254,26 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
     // The scales of a lane's row in a group of stages: bytes 2g and 2g + 1 of word i are
     // those of the two matrix steps of stage i.  Whole groups are loaded in pairs, 32 bytes
     // of a row by two lanes, and taken apart when they are needed.
-    auto scale_pair = [&](__amdgpu_buffer_rsrc_t rs, int row, int group) -> u32x4 {
-        return __builtin_amdgcn_raw_buffer_load_b128(rs, row * nblk + (group + g) * kGroupChunks, 0, 0);
+    // WORDS or not, whole words are loaded (16 bytes that start anywhere in one are taken apart by
+    // the address unit: 227 us against 254 for 7782 rows x 8192 x 4128); then a row's 32
+    // bytes end in a ninth word.
+    struct Pair {
+        u32x4 v;
+        uint32_t last;
+    };
+    auto scale_pair = [&](const Scales& sc, int row, int group) -> Pair {
+        const int at = ((sc.skip + row * nblk) & ~3) + group * kGroupChunks;
+        Pair p;
+        p.v = __builtin_amdgcn_raw_buffer_load_b128(sc.rs, at + g * kGroupChunks, 0, 0);
+        p.last = WORDS ? 0u : __builtin_amdgcn_raw_buffer_load_b32(sc.rs, at + 2 * kGroupChunks, 0, 0);
+        return p;
     };
     // What is left behind the pairs: a word for each stage, or, where rows do not start at whole
     // words, its two bytes as they stand in memory, moved to their place when taken (a move
     // here would wait for the load).  The last two of a row are read where fewer are left.
-    auto scale_rest = [&](__amdgpu_buffer_rsrc_t rs, int row, int group) -> u32x4 {
-        const uint32_t off = (uint32_t)row * (uint32_t)nblk;
+    auto scale_rest = [&](const Scales& sc, int row, int group) -> u32x4 {
+        const auto rs = sc.rs;
+        const uint32_t off = (uint32_t)sc.skip + (uint32_t)row * (uint32_t)nblk;
         u32x4 v;
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
@@ -265,17 +292,17 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
     // rows are read once, lest the line leave the L2 before its next quarter is wanted (weights
     // of 128 experts, 4096 x 4096: 1222 -> 1040 MB from memory, 176 -> 166 us for 256 rows).
     // 128 rows have no registers left for that: 288 -> 295 us (8192 rows of 64 experts).
-    constexpr int kAhead = BM <= 64 ? 4 : 1;
-    u32x4 qw[NT], qa[MT], next_qw[NT], next_qa[MT];
-    u32x4 ready_qw[kAhead][NT], flying_qw[kAhead][NT];
+    constexpr int kAhead = BM <= 64 ? (WORDS ? 4 : 2) : 1;
+    u32x4 qw[NT], qa[MT];
+    Pair next_qw[NT], next_qa[MT], ready_qw[kAhead][NT], flying_qw[kAhead][NT];
     auto load_rest = [&](int group) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int tr = wn * NT + i;
-            next_qw[i] = scale_rest(SWIGLU && (i & 1) ? rsu : rsw, weight_row(tr * 32) + r, group);
+            next_qw[i].v = scale_rest(SWIGLU && (i & 1) ? rsu : rsw, weight_row(tr * 32) + r, group);
         }
 #pragma unroll
-        for (int i = 0; i < MT; ++i) next_qa[i] = scale_rest(rsa, (wm * MT + i) * 32 + r, group);
+        for (int i = 0; i < MT; ++i) next_qa[i].v = scale_rest(rsa, (wm * MT + i) * 32 + r, group);
     };
     auto load_w_pairs = [&](int group) {
 #pragma unroll
@@ -298,18 +325,29 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
             for (int k = 1; k < kAhead; ++k) ready_qw[k - 1][i] = ready_qw[k][i];
         }
     };
-    // Both halves of a wave get the lower half's group (HALF 0) or the upper half's.
-    auto of_half = [](u32x4 v, auto half) {
+    // Both halves of a wave get the lower half's group (HALF 0) or the upper half's, from the
+    // byte on at which row r begins (rows of a tile are 32 apart, so all of its like it).
+    auto of_half = [](uint32_t v, int half) {
+        return (uint32_t)__builtin_amdgcn_permlane32_swap(v, v, false, false)[half];
+    };
+    auto group_of = [&](const Pair& p, const Scales& sc, auto half) {
+        constexpr int HALF = decltype(half)::value;
         u32x4 o;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = __builtin_amdgcn_permlane32_swap(v[i], v[i], false, false)[decltype(half)::value];
+        for (int i = 0; i < 4; ++i) o[i] = of_half(p.v[i], HALF);
+        if constexpr (!WORDS) {
+            const uint32_t behind = HALF ? p.last : of_half(p.v[0], 1);
+            const int by = (sc.skip + r * nblk) & 3;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = __builtin_amdgcn_alignbyte(i < 3 ? o[i + 1] : behind, o[i], by);
+        }
         return o;
     };
     auto take_half = [&](auto half) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) qw[i] = of_half(next_qw[i], half);
+        for (int i = 0; i < NT; ++i) qw[i] = group_of(next_qw[i], SWIGLU && (i & 1) ? rsu : rsw, half);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) qa[i] = of_half(next_qa[i], half);
+        for (int i = 0; i < MT; ++i) qa[i] = group_of(next_qa[i], rsa, half);
     };
     auto take_rest = [&](int group) {
         auto placed = [&](u32x4 v) {
@@ -324,9 +362,9 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
             return v;
         };
 #pragma unroll
-        for (int i = 0; i < NT; ++i) qw[i] = placed(next_qw[i]);
+        for (int i = 0; i < NT; ++i) qw[i] = placed(next_qw[i].v);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) qa[i] = placed(next_qa[i]);
+        for (int i = 0; i < MT; ++i) qa[i] = placed(next_qa[i].v);
     };
     uint32_t sw[NT], sa[MT];      // of one stage: bytes 0 and 1
     auto stage_scales = [&](int i) {

@@ -145,6 +145,30 @@ def test_whole_numbers_are_exact(H):
     assert torch.equal(y.cpu().double(), ref)
 
 
+@pytest.mark.parametrize("mean", [3, 50, 150])
+@pytest.mark.parametrize("H", [1024, 1056, 1120, 2144])
+@pytest.mark.parametrize("at", [(1, 0), (0, 3), (2, 2), (3, 1)])
+def test_scales_that_begin_anywhere(at, H, mean):
+    """Views whose first byte is not the first of a word, rows of 32, 33, 35 and 67 scales."""
+    g = _gen(mean + H)
+    cnt, off, rows = _compact([mean, 0, 2 * mean + 1, 7])
+    note(f"scales at {at} H={H} rows={rows}")
+    E, N = 4, 304
+    a, sa = _codes(g, (rows, H))
+    w, sw = _codes(g, (E, N, H))
+
+    def shifted(t, by):
+        flat = torch.full((t.numel() + 8,), 255, dtype=torch.uint8, device=DEV)    # NaN around it
+        flat[by:by + t.numel()] = t.to(DEV).flatten()
+        return flat[by:by + t.numel()].view(t.shape)
+    for swiglu in (False, True):
+        y = torch.full((rows, N // 2 if swiglu else N), 7.0, dtype=F32, device=DEV)
+        moe.expert_product_mxfp4(a.to(DEV), shifted(sa, at[0]), w.to(DEV), shifted(sw, at[1]), cnt.to(DEV),
+                                 off.to(DEV), swiglu=swiglu, y=y)
+        torch.cuda.synchronize()
+        _check(y, _ref(_values(a, sa), _values(w, sw), cnt, off, rows, swiglu), "shifted")
+
+
 def test_plain_product_of_odd_columns():
     """N a multiple of 8 but of no more."""
     cnt, off, rows = _compact([19, 40])

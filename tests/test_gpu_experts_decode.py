@@ -141,6 +141,22 @@ def test_scale_rows_at_any_byte(T, H, I, E, K, out):
     _check(y, _ref(x.double(), idx, w, w13[2], w2[2], 3 if out == F32 else 2), "scales")
 
 
+@pytest.mark.parametrize("H,I", [(1024, 128), (96, 800), (2144, 1056)])
+@pytest.mark.parametrize("at", [1, 2, 3])
+def test_scales_that_begin_anywhere(at, H, I):
+    note(f"decode scales at {at} H={H} I={I}")
+    x, idx, w, w13, w2 = _inputs(5, H, I, 6, 2, True, H + at)
+
+    def shifted(t):
+        flat = torch.full((t.numel() + 8,), 255, dtype=torch.uint8, device=DEV)    # NaN around it
+        flat[at:at + t.numel()] = t.to(DEV).flatten()
+        return flat[at:at + t.numel()].view(t.shape)
+    y = moe.experts_decode(x.to(DEV), idx.to(DEV), w.to(DEV), w13[0].to(DEV), w2[0].to(DEV),
+                           shifted(w13[1]), shifted(w2[1]), out_dtype=F32)
+    torch.cuda.synchronize()
+    _check(y, _ref(x.double(), idx, w, w13[2], w2[2], 3), "shifted")
+
+
 @pytest.mark.parametrize("out", [BF16, F32])
 @pytest.mark.parametrize("T,K", [(5, 1), (11, 1), (20, 4), (33, 2)])
 def test_many_entries_of_one_expert_among_many(T, K, out):

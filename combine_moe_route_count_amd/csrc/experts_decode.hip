@@ -340,7 +340,15 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
             return;
         }
     } else {
-        for (int i = threadIdx.x; i < list_words(N); i += kThreads) list_block[i] = lists[i];
+        // (lists that another call on the same workspace has overwritten give wrong results, but
+        // no address out of range: what is used as an index is bounded here and in entry())
+        auto bounded = [&](int i, uint32_t v) {
+            return i == 0 ? min(v, (uint32_t)N) : i >= 2 && i < 2 + N ? min(v, (uint32_t)a.E - 1) : v;
+        };
+        for (int i = threadIdx.x; i < list_words(N); i += kThreads) {
+            const uint32_t v = lists[i];
+            list_block[i] = bounded(2 * i, v & 0xffffu) | bounded(2 * i + 1, v >> 16) << 16;
+        }
         __syncthreads();
     }
     const int lane = threadIdx.x % kWave;
@@ -360,6 +368,7 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
         slot = item / blocks;
         return (int64_t)(item - slot * blocks) * S::kRows;
     };
+    auto entry = [&](int at) { return UP ? (int)l.ent[at] : min((int)l.ent[at], N - 1); };
     auto seek = [&](int item, Cursor<S::kLoadsB>& c) {
         int slot;
         const int64_t r0 = item_rows(item, slot);
@@ -374,7 +383,7 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
             // (of PACK, column col is part col / width of entry col % width)
             const int part = PACK ? col / S::kWidth : 0, of = PACK ? col % S::kWidth : col;
             const bool none = of >= n || part >= P;
-            const int f = l.ent[first + (none ? 0 : of)];
+            const int f = entry(first + (none ? 0 : of));
             const int64_t row = (UP ? f / a.K : f) + (int64_t)(none ? 0 : part) * N;
             c.col[i] = (uint32_t)(row * K * 2) | outside_if(none);
         }
@@ -569,7 +578,7 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
             const int col = c * 16 + r;
-            const int f = l.ent[first + (col < n ? col : 0)];
+            const int f = entry(first + (col < n ? col : 0));
             if constexpr (UP) {
                 const int64_t i = r0 + row_wave * 16 + 4 * g;
                 float v[4];

@@ -48,6 +48,7 @@ using LdsWords = __attribute__((address_space(3))) u32x4;
 
 constexpr int kMaxEntries = kDecodeEntries;
 constexpr int kGroup = 4;      // stages in LDS
+constexpr float kBf16Max = 0x1.fep127f;
 
 // The work of one pass over an expert's weights: up to `width` of its entries.  Slot s
 // belongs to expert[s] and has the entries ent[first[s]] .. ent[first[s + 1] - 1].  All
@@ -585,12 +586,20 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[q] = silu_of(acc[0][c][q]) * acc[1][c][q];
                 for (int p = 0; p < h_parts; ++p) {
-                    const u32x2 b = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    // a finite h past bf16's largest value has that as its first part; an infinity
+                    // or a NaN stands in the first part alone
+                    float part[4];
+                    bool finite[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        finite[q] = __builtin_isfinite(v[q]);
+                        part[q] = finite[q] ? __builtin_amdgcn_fmed3f(v[q], -kBf16Max, kBf16Max) : v[q];
+                    }
+                    const u32x2 b = {pack_bf16x2(part[0], part[1]), pack_bf16x2(part[2], part[3])};
                     if (col < n && i < M) *(u32x2*)(h + p * h_part + f * a.I + i) = b;
                     const float was[4] = {bf16lo(b[0]), bf16hi(b[0]), bf16lo(b[1]), bf16hi(b[1])};
-                    // an infinity or a NaN stands in the first part alone
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] = __builtin_isfinite(v[q]) ? v[q] - was[q] : 0.0f;
+                    for (int q = 0; q < 4; ++q) v[q] = finite[q] ? v[q] - was[q] : 0.0f;
                 }
             } else {
 #pragma unroll

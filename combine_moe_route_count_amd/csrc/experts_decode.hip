@@ -460,12 +460,23 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
         return o;
     };
 
-    f32x4 acc[2][NT];
+    // The further parts of h have sums of their own: where a weight is infinite the first part's
+    // sum is the result (0 or the other sign, which a further part may have, would make it NaN).
+    constexpr int kSums = kParts > 1 ? 2 : 1;
+    f32x4 sum[kSums][2][NT];
+    auto& acc = sum[0];
     auto clear = [&] {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int k = 0; k < kSums; ++k)
 #pragma unroll
-            for (int c = 0; c < NT; ++c) acc[i][c] = f32x4{0, 0, 0, 0};
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < NT; ++c) sum[k][i][c] = f32x4{0, 0, 0, 0};
+    };
+    auto with_rest = [](f32x4 first, f32x4 rest) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) first[q] = __builtin_isfinite(first[q]) ? first[q] + rest[q] : first[q];
+        return first;
     };
     u32x4 scales[2] = {};
     uint32_t scale[2][S::kWords] = {};
@@ -501,7 +512,8 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
                             const bf16x8 b = other(p, c, part * 16 + 4 * g + q);
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
-                                acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], b, acc[i][c], 0, 0, 0);
+                                sum[p > 0][i][c] =
+                                    __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], b, sum[p > 0][i][c], 0, 0, 0);
                         }
                 }
             }
@@ -519,7 +531,8 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
                         const bf16x8 b = other(p, c, 4 * q + g);
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            acc[i][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], b, acc[i][c], 0, 0, 0);
+                            sum[p > 0][i][c] =
+                                __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], b, sum[p > 0][i][c], 0, 0, 0);
                     }
             }
         }
@@ -569,12 +582,19 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
         if constexpr (PACK) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const f32x4 own = acc[i][0];
+                f32x4 rest = {0, 0, 0, 0};
 #pragma unroll
                 for (int p = 1; p < P; ++p)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[i][0][q] += __shfl_down(own[q], p * S::kWidth);
+                    for (int q = 0; q < 4; ++q) rest[q] += __shfl_down(acc[i][0][q], p * S::kWidth);
+                acc[i][0] = with_rest(acc[i][0], rest);
             }
+        }
+        if constexpr (kSums > 1) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < NT; ++c) acc[i][c] = with_rest(acc[i][c], sum[1][i][c]);
         }
 #pragma unroll
         for (int c = 0; c < NT; ++c) {

@@ -1,5 +1,5 @@
 """GPU tests of experts_decode where its numbers end: an h between the products that bf16
-does not reach, and infinities.
+does not reach, and infinities among the weights.
 
 h goes through the second product in bf16 parts.  Every h here is a sum of few powers of
 two, so each is known exactly: with silu(g) = g for g >= 64 (1 / (1 + exp(-64)) rounds to 1
@@ -73,6 +73,39 @@ def test_h_past_the_largest_bf16(mx, T, E, I, sign, out):
     got = _call(x, idx, torch.ones((T, 1)), w13, w2, out)
     want = torch.tensor([sign * (1 if r % 3 else -1) * 2.0 ** (94 - r % 8) * (1 - 2.0 ** -10) for r in range(H)])
     assert torch.equal(got, want.to(out).expand(T, H))
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("T,E,I", SIZES)
+@pytest.mark.parametrize("mx", [False, True])
+def test_infinite_weights_of_the_second_product(mx, T, E, I, out):
+    """A weight that is infinite gives an infinity of its and h's sign, whether h is a bf16 number
+    (1: its further parts are 0) or lies above or below one (1 +- 2^-10); with h = 0 a NaN.  Rows
+    without such a weight are what they are."""
+    note(f"decode infinite weights mx={mx} T={T} I={I} {out}")
+    x = torch.zeros((T, H), dtype=BF16)
+    x[:, 0] = x[:, 32] = 1
+    w13, w2 = Weights(E, 2 * I, H, mx), Weights(E, H, I, mx)
+    h = [1.0, 1 + 2.0 ** -10, 1 - 2.0 ** -10, -1.0, -1 - 2.0 ** -10, -1 + 2.0 ** -10, 0.0]
+    for i, v in enumerate(h):
+        w13.put(i, 0, 6)                                        # g = 64
+        if v:
+            w13.put(I + i, 0, -6, 1 if v > 0 else -1)
+        if abs(v) not in (0.0, 1.0):
+            w13.put(I + i, 32, -16, 1 if v > 1 or -1 < v < 0 else -1)
+    want = torch.zeros(H)
+    for i, v in enumerate(h):
+        for j, sign in enumerate((1, -1)):
+            w2.put(2 * i + j, i, INF, sign)
+            want[2 * i + j] = sign * v * INF                    # 0 * infinity is NaN here too
+    w2.put(20, 0, 3)
+    want[20] = 8
+    w2.put(21, 4, 1, -1)
+    want[21] = 2 + 2.0 ** -9
+    idx = (torch.arange(T) % E).int().unsqueeze(1)
+    got = _call(x, idx, torch.ones((T, 1)), w13, w2, out)
+    assert torch.equal(got.nan_to_num(nan=7.0, posinf=INF, neginf=-INF),
+                       want.to(out).nan_to_num(nan=7.0, posinf=INF, neginf=-INF).expand(T, H))
 
 
 @pytest.mark.parametrize("T,E,I", SIZES)

@@ -33,7 +33,7 @@
 #include <type_traits>
 
 #include "train_device.hpp"
-#include "experts.hpp"
+#include "experts_device.hpp"
 #include "internal.hpp"
 
 namespace moe {
@@ -248,11 +248,6 @@ __device__ __forceinline__ uint32_t widen2(uint32_t d, float scale) {
 
 __device__ __forceinline__ u32x4 widen8(uint32_t d, float scale) {
     return u32x4{widen2<0>(d, scale), widen2<1>(d, scale), widen2<2>(d, scale), widen2<3>(d, scale)};
-}
-
-__device__ __forceinline__ float silu_of(float g) {
-    // g / (1 + exp(-g)); exp overflows to an infinity below -88, where the quotient is -0
-    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
 }
 
 // Ored to an offset below 2^31 it leaves every descriptor's range (2^31 at the most).

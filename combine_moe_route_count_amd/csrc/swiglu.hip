@@ -4,8 +4,6 @@
 // A row of gu holds I gate values g and then I up values u:
 //   h = silu(g) * u,  silu(g) = g * s,  s = 1 / (1 + exp(-g))
 //   dg = dh * u * s * (1 + g * (1 - s)),  du = dh * silu(g)
-// With t = exp(-|g|) and r = 1 / (1 + t), {s, 1 - s} is {r, t*r} or, for g < 0,
-// {t*r, r}: no step overflows and 1 - s keeps its digits where s is near 1.
 //
 // The 8-bit checkpoint of gu: e4m3 codes, one f32 scale per 128 elements of a row, the
 // smallest power of two that keeps the block's largest finite magnitude within 448.
@@ -23,31 +21,13 @@
 #include <type_traits>
 
 #include "train_device.hpp"
-#include "experts.hpp"
+#include "experts_device.hpp"
 
 namespace moe {
 
 namespace {
 
 constexpr int kThreads = 256;
-
-struct Act {
-    float s, c;   // sigmoid and 1 - sigmoid
-};
-
-__device__ __forceinline__ Act sigmoid_of(float g) {
-    // exp(-|g|) = 2^(p + q) with p the rounded product -|g| * log2 e and q what it
-    // lost, so large |g| keep their digits
-    const float a = -fabsf(g);
-    constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596299e-8f;
-    const float p = a * kLog2e;
-    const float q = __builtin_fmaf(a, kLog2e, -p) + a * kLog2eLow;
-    const float e = __builtin_amdgcn_exp2f(p);
-    const float t = a < -200.0f ? 0.0f : __builtin_fmaf(e * q, 0.693147182f, e);
-    const float r = __builtin_amdgcn_rcpf(1.0f + t);
-    const float tr = t * r;
-    return g < 0.0f ? Act{tr, r} : Act{r, tr};
-}
 
 // Whether a segment owns row r: the last expert e whose segment starts at or before r
 // has r - off[e] < cnt[e].
@@ -210,7 +190,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(SwigluArgs a, int log_
                 }
             }
 #pragma unroll
-            for (int j = 0; j < EL; ++j) h[j] = g[j] * sigmoid_of(g[j]).s * up[j];
+            for (int j = 0; j < EL; ++j) h[j] = silu_of(g[j]) * up[j];
             store_unit<HF32, true>(a.h, r * a.I + col, h);
         }
     }

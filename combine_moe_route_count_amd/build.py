@@ -19,8 +19,9 @@ SOURCES = ["api.cpp", "geometry.cpp", "route.hip", "scatter.hip", "combine.hip",
            "scratch.hip", "api_train.cpp", "gate.hip", "grad.hip", "embedding.hip",
            "api_experts.cpp", "mxfp4.hip", "swiglu.hip", "expert_product.hip",
            "experts_decode.hip"]
-HEADERS = ["api_common.hpp", "device_common.hpp", "experts.hpp", "experts_device.hpp", "internal.hpp",
-           "route_device.hpp", "rows_device.hpp", "train.hpp", "train_device.hpp"]
+HEADERS = ["api_common.hpp", "device_common.hpp", "experts.hpp", "experts_device.hpp",
+           "experts_rules.hpp", "internal.hpp", "route_device.hpp", "rows_device.hpp", "train.hpp",
+           "train_device.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -7,6 +7,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "experts_rules.hpp"
 #include "train.hpp"
 
 namespace moe {

@@ -50,17 +50,15 @@ constexpr int kMaxEntries = kDecodeEntries;
 constexpr int kGroup = 4;      // stages in LDS
 constexpr float kBf16Max = 0x1.fep127f;
 
-// The work of one pass over an expert's weights: up to `width` of its entries.  Slot s
-// belongs to expert[s] and has the entries ent[first[s]] .. ent[first[s + 1] - 1].  All
-// three are arrays of one block of 16-bit words, sized by the number of entries, so that
-// few entries leave the LDS to the stages.
+// A block of lists (ListLayout), sized by the number of entries, so that few of them leave the LDS
+// to the stages.
 struct Lists {
     uint16_t *n, *expert, *first, *ent;
     __device__ __forceinline__ Lists(uint16_t* base, int N)
-        : n(base), expert(base + 2), first(base + 2 + N), ent(base + 4 + 2 * N) {}
+        : n(base), expert(base + ListLayout{N}.expert()), first(base + ListLayout{N}.first()),
+          ent(base + ListLayout{N}.ent()) {}
 };
-__host__ __device__ constexpr int list_words(int64_t N) { return (int)(4 + 3 * N + 1) / 2; }   // of 32 bits
-constexpr size_t kListBytes = (list_words(kMaxEntries) * 4 + 255) / 256 * 256;
+constexpr size_t kListBytes = (ListLayout{kMaxEntries}.words32() * 4 + 255) / 256 * 256;
 
 // Scratch of build_lists: how many entries of each expert a chunk of 64 entries has (16
 // chunks, 64 at the most), in four arrays of 256 experts each, and sums of the waves.
@@ -178,7 +176,8 @@ __device__ void build_lists(const int32_t* idx, int N, int E, int width, const L
 }
 
 // The same for at most 64 entries, by one wave on its own (experts in the order of their
-// first entries): 7 barriers and the passes over the experts' counts cost 4 us more.
+// first entries): the barriers of build_lists and its passes over the experts' counts cost 4 us
+// more.
 __device__ void build_short_lists(const int32_t* idx, int N, int E, int width, const Lists& l) {
     const int lane = threadIdx.x % kWave;
     int e = lane < N ? idx[lane] : -1;
@@ -337,13 +336,11 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
         }
     } else {
         // (lists that another call on the same workspace has overwritten give wrong results, but
-        // no address out of range: what is used as an index is bounded here and in entry())
-        auto bounded = [&](int i, uint32_t v) {
-            return i == 0 ? min(v, (uint32_t)N) : i >= 2 && i < 2 + N ? min(v, (uint32_t)a.E - 1) : v;
-        };
-        for (int i = threadIdx.x; i < list_words(N); i += kThreads) {
+        // no index or address out of range)
+        const ListLayout lay{N};
+        for (int i = threadIdx.x; i < lay.words32(); i += kThreads) {
             const uint32_t v = lists[i];
-            list_block[i] = bounded(2 * i, v & 0xffffu) | bounded(2 * i + 1, v >> 16) << 16;
+            list_block[i] = lay.bounded(2 * i, v & 0xffffu, a.E) | lay.bounded(2 * i + 1, v >> 16, a.E) << 16;
         }
         __syncthreads();
     }
@@ -364,7 +361,6 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
         slot = item / blocks;
         return (int64_t)(item - slot * blocks) * S::kRows;
     };
-    auto entry = [&](int at) { return UP ? (int)l.ent[at] : min((int)l.ent[at], N - 1); };
     auto seek = [&](int item, Cursor<S::kLoadsB>& c) {
         int slot;
         const int64_t r0 = item_rows(item, slot);
@@ -379,7 +375,7 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
             // (of PACK, column col is part col / width of entry col % width)
             const int part = PACK ? col / S::kWidth : 0, of = PACK ? col % S::kWidth : col;
             const bool none = of >= n || part >= P;
-            const int f = entry(first + (none ? 0 : of));
+            const int f = l.ent[none ? 0 : first + of];
             const int64_t row = (UP ? f / a.K : f) + (int64_t)(none ? 0 : part) * N;
             c.col[i] = (uint32_t)(row * K * 2) | outside_if(none);
         }
@@ -594,7 +590,7 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
             const int col = c * 16 + r;
-            const int f = entry(first + (col < n ? col : 0));
+            const int f = l.ent[col < n ? first + col : 0];
             if constexpr (UP) {
                 const int64_t i = r0 + row_wave * 16 + 4 * g;
                 float v[4];
@@ -745,7 +741,7 @@ hipError_t launch(const DecodeArgs& a, const Work& w, hipStream_t s) {
     using S = Stream<MX, UP, P, NT, SK, WAVES, SPLIT, PACK>;
     const int64_t N = a.T * a.K, M = UP ? a.I : a.H;
     const int64_t most = N * ((M + S::kRows - 1) / S::kRows);
-    const size_t lists_lds = (size_t)list_words(N) * 4;
+    const size_t lists_lds = (size_t)ListLayout{(int)N}.words32() * 4;
     const int per_cu = (int)(kLdsPerCu / (kGroup * S::kStageBytes + (SPLIT ? (WAVES - 1) * NT * 2048 : 16) + lists_lds));
     const int64_t fit = (int64_t)256 * (per_cu < 1 ? 1 : per_cu);
     // Weights go past the caches where rows are whole lines; a line that two stages share would be

@@ -464,10 +464,22 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
 #pragma unroll
                 for (int c = 0; c < NT; ++c) sum[k][i][c] = f32x4{0, 0, 0, 0};
     };
-    auto with_rest = [](f32x4 first, f32x4 rest) {
+    // first + rest, but first where that is infinite.
+    auto add_rest = [](f32x4 (&first)[NT], const f32x4 (&rest)[NT]) {
+        float most = 0.0f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) first[q] = __builtin_isfinite(first[q]) ? first[q] + rest[q] : first[q];
-        return first;
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) most = fmaxf(most, fabsf(first[c][q]));
+        if (ballot64(most == __builtin_inff())) {     // rare
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) first[c][q] += __builtin_isinf(first[c][q]) ? 0.0f : rest[c][q];
+        } else {
+#pragma unroll
+            for (int c = 0; c < NT; ++c) first[c] += rest[c];
+        }
     };
     u32x4 scales[2] = {};
     uint32_t scale[2][S::kWords] = {};
@@ -573,19 +585,19 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
         if constexpr (PACK) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                f32x4 rest = {0, 0, 0, 0};
+                f32x4 rest[NT];
 #pragma unroll
-                for (int p = 1; p < P; ++p)
+                for (int q = 0; q < 4; ++q) {
+                    rest[0][q] = __shfl_down(acc[i][0][q], S::kWidth);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) rest[q] += __shfl_down(acc[i][0][q], p * S::kWidth);
-                acc[i][0] = with_rest(acc[i][0], rest);
+                    for (int p = 2; p < P; ++p) rest[0][q] += __shfl_down(acc[i][0][q], p * S::kWidth);
+                }
+                add_rest(acc[i], rest);
             }
         }
         if constexpr (kSums > 1) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int c = 0; c < NT; ++c) acc[i][c] = with_rest(acc[i][c], sum[1][i][c]);
+            for (int i = 0; i < 2; ++i) add_rest(acc[i], sum[1][i]);
         }
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
@@ -593,9 +605,12 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
             const int f = l.ent[col < n ? first + col : 0];
             if constexpr (UP) {
                 const int64_t i = r0 + row_wave * 16 + 4 * g;
+                // (constants over the whole kernel: 237 -> 248 us, 32 tokens of 128 experts in MXFP4)
+                const ExpConstants constants = ExpConstants::here();
+                const float most = constant_here(kBf16Max);
                 float v[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = silu_of(acc[0][c][q]) * acc[1][c][q];
+                for (int q = 0; q < 4; ++q) v[q] = silu_of(acc[0][c][q], constants) * acc[1][c][q];
                 for (int p = 0; p < h_parts; ++p) {
                     // a finite h past bf16's largest value has that as its first part; an infinity
                     // or a NaN stands in the first part alone
@@ -604,7 +619,7 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         finite[q] = __builtin_isfinite(v[q]);
-                        part[q] = finite[q] ? __builtin_amdgcn_fmed3f(v[q], -kBf16Max, kBf16Max) : v[q];
+                        part[q] = finite[q] ? __builtin_amdgcn_fmed3f(v[q], -most, most) : v[q];
                     }
                     const u32x2 b = {pack_bf16x2(part[0], part[1]), pack_bf16x2(part[2], part[3])};
                     if (col < n && i < M) *(u32x2*)(h + p * h_part + f * a.I + i) = b;

@@ -48,7 +48,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kBN = 256;          // weight rows of a tile
+constexpr int kBN = kTileCols;    // weight rows of a tile
 constexpr int kStageChunks = 4;   // 16-byte chunks of a row in a stage: 128 codes
 constexpr int kStageBytes = 64;
 constexpr int kGroup = 4;         // stages in LDS, and stages whose scales are loaded together
@@ -578,13 +578,11 @@ __global__ __launch_bounds__(kThreads, (BM <= 64 ? 2 : 1)) void product_kernel(P
 // joined, in the order of the waves.  One row by 8192 x 8192 takes 14.2 us, 2.5 TB/s: the
 // latency of 16 stages a wave and the launch (21.5 with tiles of 64 rows by 256).
 // ---------------------------------------------------------------------------
-constexpr int kNarrowRows = 32, kNarrowBN = 64;
-
 template <bool SWIGLU, bool WORDS>
 __global__ __launch_bounds__(kThreads, 1) void product_narrow_kernel(ProductArgs a, int col_tiles,
                                                                      int64_t base) {
     constexpr int kA = kNarrowRows * kStageBytes;
-    constexpr int kStage = kA + kNarrowBN * kStageBytes;
+    constexpr int kStage = kA + kNarrowCols * kStageBytes;
     __shared__ __align__(16) uint8_t lds0[kWaves * kStage], lds1[kWaves * kStage];
     __shared__ __align__(16) uint8_t lds2[kWaves * kStage], lds3[kWaves * kStage];
     int col = 0;
@@ -602,7 +600,7 @@ __global__ __launch_bounds__(kThreads, 1) void product_narrow_kernel(ProductArgs
     const int per = (stages + kWaves - 1) / kWaves;
     const int s0 = min(wave * per, stages), s1 = min(s0 + per, stages);     // the wave's
     const int64_t NO = SWIGLU ? a.N / 2 : a.N;
-    constexpr int kCols = SWIGLU ? kNarrowBN / 2 : kNarrowBN;
+    constexpr int kCols = SWIGLU ? kNarrowCols / 2 : kNarrowCols;
     const int64_t n0 = (int64_t)col * kCols;
     const int64_t wrow = (int64_t)t.e * a.N + n0;
     const int wrows = (int)(NO - n0 < kCols ? NO - n0 : kCols);
@@ -713,7 +711,7 @@ __global__ __launch_bounds__(kThreads, 1) void product_narrow_kernel(ProductArgs
     __syncthreads();
 
     // each wave's sums, row by row of y, in one buffer
-    constexpr int kPitch = kNarrowBN + 4;
+    constexpr int kPitch = kNarrowCols + 4;
     static_assert(kNarrowRows * kPitch * 4 <= sizeof(lds0), "a wave's sums fit one buffer");
     float* turn = (float*)(wave == 0 ? lds0 : wave == 1 ? lds1 : wave == 2 ? lds2 : lds3);
 #pragma unroll
@@ -775,27 +773,12 @@ bool whole_words(const ProductArgs& a) {
 
 hipError_t launch_product(const ProductArgs& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
-    // Tile heights 64, 128, 256 by the mean rows of an expert, in us (32 experts with uneven
-    // loads, 4096 x 4096): mean 24 62, 64, 72; 64 73, 75, 82; 96 91, 90, 94; 192 135, 117, 122;
-    // 256 163, 148, 128; 384 224, 200, 185.
-    // A height whose tiles would leave 100 CUs without one gives way to the next lower, in us:
-    // 120 tiles of 256 rows 22.2 against 16.9 with 128, 136 35.7 and 28.4, 168 23.6 and 27.6,
-    // 184 37.3 and 44.9; 138 tiles of 128 rows 22.5 against 20.2 with 64, 144 22.8 and 20.8,
-    // 184 24.9 and 31.2, 192 26.4 and 31.9.
-    // Narrow tiles where nearly each can have a CU, in us against tiles of 64 rows: 56 of them 9.0
-    // and 17.8, 160 11.6 and 16.1, 256 17.9 and 27.6, 264 17.2 and 27.2; 320 20.3 and 16.4,
-    // 512 31.5 and 27.8.
-    const int64_t used = a.E < a.rows ? a.E : a.rows;
-    auto tiles = [&](int64_t height, int64_t width) {       // about
-        const int64_t row_tiles = (2 * a.rows / height + used) / 2;
-        return (row_tiles > used ? row_tiles : used) * ((a.N + width - 1) / width);
-    };
-    constexpr int64_t kCUs = 256, kIdle = 100;
-    const int64_t mean = a.rows / a.E;
-    if (tiles(kNarrowRows, kNarrowBN) <= kCUs + kCUs / 8) MOE_PRODUCT(kNarrowRows, kNarrowBN, product_narrow_kernel);
-    else if (mean <= 64 || tiles(128, kBN) < kCUs - kIdle) MOE_PRODUCT(64, kBN, product_kernel, 64 MOE_COMMA);
-    else if (mean < 224 || tiles(256, kBN) < kCUs - kIdle) MOE_PRODUCT(128, kBN, product_kernel, 128 MOE_COMMA);
-    else MOE_PRODUCT(256, kBN, product_kernel, 256 MOE_COMMA);
+    switch (ProductSize{a.rows, a.N, a.E}.tile_rows()) {
+        case kNarrowRows: MOE_PRODUCT(kNarrowRows, kNarrowCols, product_narrow_kernel); break;
+        case 64: MOE_PRODUCT(64, kTileCols, product_kernel, 64 MOE_COMMA); break;
+        case 128: MOE_PRODUCT(128, kTileCols, product_kernel, 128 MOE_COMMA); break;
+        default: MOE_PRODUCT(256, kTileCols, product_kernel, 256 MOE_COMMA);
+    }
     return hipGetLastError();
 }
 

@@ -5,6 +5,8 @@ import subprocess
 
 import pytest
 
+import _experts_forms as F
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(os.path.dirname(HERE), "combine_moe_route_count_amd", "csrc")
 
@@ -80,3 +82,29 @@ def test_lists_in_order_are_kept(lists, N, E):
     words += [0] * (_size(N) - len(words))
     _, got = lists(N, E, words)
     assert got == words
+
+
+RULES = r"""
+#include <cstdio>
+#include "experts_rules.hpp"
+int main() {   // "p rows E N"
+    char what;
+    while (std::scanf(" %c", &what) == 1) {
+        long a, b;
+        int d;
+        if (std::scanf("%ld %d %ld", &a, &d, &b) != 3) return 1;
+        std::printf("%d\n", moe::ProductSize{a, b, d}.tile_rows());
+    }
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def rules(tmp_path_factory):
+    run = _compile(tmp_path_factory.mktemp("rules"), RULES)
+    return lambda lines: [[int(v) for v in l.split()] for l in run("\n".join(lines)).splitlines()]
+
+
+def test_tested_products_reach_their_tiles(rules):
+    for height, sizes in F.PRODUCT.items():
+        assert rules(["p %d %d %d" % s for s in sizes]) == [[height]] * len(sizes), height

@@ -742,12 +742,11 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(DecodeArgs a, const 
 
 struct Work {
     uint32_t* lists;
-    int down_width;       // entries that the second product takes at a time
     uint16_t* h;
     int64_t h_part;       // elements of a part
     float* y;
     int parts;            // of h
-    bool split, pack;     // SPLIT of the first product, PACK of the second
+    StreamForm up, down;
 };
 
 // Workgroups: as many as fit the card at once (LDS decides), or one per item.
@@ -758,7 +757,7 @@ hipError_t launch(const DecodeArgs& a, const Work& w, hipStream_t s) {
     const int64_t most = N * ((M + S::kRows - 1) / S::kRows);
     const size_t lists_lds = (size_t)ListLayout{(int)N}.words32() * 4;
     const int per_cu = (int)(kLdsPerCu / (kGroup * S::kStageBytes + (SPLIT ? (WAVES - 1) * NT * 2048 : 16) + lists_lds));
-    const int64_t fit = (int64_t)256 * (per_cu < 1 ? 1 : per_cu);
+    const int64_t fit = (int64_t)kCUs * (per_cu < 1 ? 1 : per_cu);
     // Weights go past the caches where rows are whole lines; a line that two stages share would be
     // fetched twice: 640 us with, 707 without (32 tokens, bf16, 128 experts of 2816 x 2816), 889
     // and 761 (2888 x 2888).
@@ -768,84 +767,64 @@ hipError_t launch(const DecodeArgs& a, const Work& w, hipStream_t s) {
     const dim3 grid((unsigned)((most < fit ? most : fit) + (UP ? 1 : 0)));
     if (S::kLine && once)
         stream_kernel<MX, UP, P, NT, SK, WAVES, SPLIT, PACK, S::kLine>
-            <<<grid, S::kThreads, lists_lds, s>>>(a, w.lists, w.down_width, w.h, w.h_part, w.y, w.parts);
+            <<<grid, S::kThreads, lists_lds, s>>>(a, w.lists, w.down.width, w.h, w.h_part, w.y, w.parts);
     else
         stream_kernel<MX, UP, P, NT, SK, WAVES, SPLIT, PACK, false>
-            <<<grid, S::kThreads, lists_lds, s>>>(a, w.lists, w.down_width, w.h, w.h_part, w.y, w.parts);
+            <<<grid, S::kThreads, lists_lds, s>>>(a, w.lists, w.down.width, w.h, w.h_part, w.y, w.parts);
     return hipGetLastError();
-}
-
-// Slots that the entries of the experts in use fill, about.
-int64_t slots_of(const DecodeArgs& a, int width) {
-    const int64_t N = a.T * a.K, used = N < a.E ? N : a.E, full = (2 * N / width + used) / 2;
-    return full > used ? full : used;
 }
 
 template <bool MX, bool UP, int P, int NT, int SK, bool PACK = false>
 hipError_t launch_waves(const DecodeArgs& a, const Work& w, hipStream_t s) {
-    const int64_t N = a.T * a.K, used = N < a.E ? N : a.E, M = UP ? a.I : a.H;
-    // 4 waves share the entries' rows; 2 where 4 would leave CUs without work
-    if (used * ((M + (UP ? 63 : 127)) / (UP ? 64 : 128)) >= 512)
-        return launch<MX, UP, P, NT, SK, 4, false, PACK>(a, w, s);
-    return launch<MX, UP, P, NT, SK, 2, false, PACK>(a, w, s);
+    return (UP ? w.up : w.down).waves == 4 ? launch<MX, UP, P, NT, SK, 4, false, PACK>(a, w, s)
+                                           : launch<MX, UP, P, NT, SK, 2, false, PACK>(a, w, s);
 }
 
-template <bool MX, bool UP, int P, int NT>
-hipError_t launch_stage(const DecodeArgs& a, const Work& w, hipStream_t s) {
-    if constexpr (UP && NT == 1)
-        if (w.split) return launch<MX, UP, P, NT, MX ? 128 : 64, 4, true, false>(a, w, s);
-    // Whole cache lines of MXFP4 rows (stages of 256) where a group of stages is not mostly zeros:
-    // 163 -> 152 us (111 experts' W1 and W3 of 1024 x 7168), 238 -> 226 both products (32 tokens).
-    // Not with the parts of h apart: their stages leave the CU one workgroup, 97 -> 114 us (W2).
-    constexpr int kLong = 768;
-    if constexpr (!UP && NT == 1 && MX)
-        if (w.pack)
-            return a.I >= kLong ? launch_waves<MX, UP, P, NT, 256, true>(a, w, s)
-                                : launch_waves<MX, UP, P, NT, 128, true>(a, w, s);
-    if constexpr (!MX) {
-        return launch_waves<MX, UP, P, NT, 64>(a, w, s);
+template <bool MX>
+hipError_t launch_up(const DecodeArgs& a, const Work& w, hipStream_t s) {
+    constexpr int kShort = MX ? 128 : 64;
+    if (w.up.split) return launch<MX, true, 1, 1, kShort, 4, true, false>(a, w, s);
+    if constexpr (MX) {
+        if (w.up.width == 32) return launch<MX, true, 1, 2, kShort, 4, false, false>(a, w, s);
+        if (w.up.stage == 256) return launch_waves<MX, true, 1, 1, 256>(a, w, s);
     } else {
-        if constexpr (NT == 1 && P == 1)
-            if (a.H >= kLong) return launch_waves<MX, UP, P, NT, 256>(a, w, s);
-        return launch_waves<MX, UP, P, NT, 128>(a, w, s);
+        if (w.up.width == 32) return launch_waves<MX, true, 1, 2, kShort>(a, w, s);
     }
+    return launch_waves<MX, true, 1, 1, kShort>(a, w, s);
 }
 
-template <bool MX, int P, int NT>
-hipError_t launch_all(const DecodeArgs& a, bool split, hipStream_t s) {
+template <bool MX, int P>
+hipError_t launch_down(const DecodeArgs& a, const Work& w, hipStream_t s) {
+    constexpr int kShort = MX ? 128 : 64;
+    if constexpr (MX) {
+        if (w.down.pack)
+            return w.down.stage == 256 ? launch_waves<MX, false, P, 1, 256, true>(a, w, s)
+                                       : launch_waves<MX, false, P, 1, 128, true>(a, w, s);
+        if (w.down.width == 32) return launch<MX, false, P, 2, kShort, 4, false, false>(a, w, s);
+    } else {
+        if (w.down.width == 32) return launch_waves<MX, false, P, 2, kShort>(a, w, s);
+    }
+    return launch_waves<MX, false, P, 1, kShort>(a, w, s);
+}
+
+template <bool MX>
+hipError_t launch_type(const DecodeArgs& a, hipStream_t s) {
     const int64_t N = a.T * a.K;
     Work w{};
     w.lists = (uint32_t*)a.ws;
     w.y = (float*)((char*)a.ws + kListBytes);
     w.h = (uint16_t*)(w.y + N * a.H);
     w.h_part = N * a.I;
-    w.parts = P;
-    w.split = split;
-    // Parts as columns, in us without and with, by entries per expert: one token of 8 experts 49.1,
-    // 45.2 (4 experts a token, f32 result 49.4, 43.8); 2 240, 238 (f32 result 261, 240); 4 272, 270; 8
-    // 290, 298, where some experts have too many for one pass.  (The parts are read by one
-    // descriptor of less than 2^31 bytes.)
-    w.pack = MX && NT == 1 && N <= 4 * (int64_t)a.E && w.h_part * 2 * P < ((int64_t)1 << 31);
-    w.down_width = w.pack ? 16 / P : 16 * NT;
-    hipError_t st = launch_stage<MX, true, 1, NT>(a, w, s);
-    if (st == hipSuccess) st = launch_stage<MX, false, P, NT>(a, w, s);
+    w.parts = a.out_f32 ? 3 : 2;
+    const DecodeSize size{a.T, a.H, a.I, a.K, a.E, MX, w.parts};
+    w.up = size.up();
+    w.down = size.down();
+    hipError_t st = launch_up<MX>(a, w, s);
+    if (st == hipSuccess) st = a.out_f32 ? launch_down<MX, 3>(a, w, s) : launch_down<MX, 2>(a, w, s);
     if (st != hipSuccess) return st;
     const dim3 grid((unsigned)((a.H + 4 * kJoinThreads - 1) / (4 * kJoinThreads)), (unsigned)a.T);
     join_kernel<<<grid, kJoinThreads, 0, s>>>(a, w.y);
     return hipGetLastError();
-}
-
-template <bool MX>
-hipError_t launch_type(const DecodeArgs& a, hipStream_t s) {
-    // The first product's K is split over the waves where that still leaves a CU no more than
-    // two items, in us without and with: bf16 64 items 26.3, 18.5, 256 35.0, 28.4, 512 40.6,
-    // 39.1, 1088 40.2, 56.2; MXFP4 36 items 47.0, 26.3, 128 23.5, 17.9, 320 33.5, 25.3, 512
-    // 26.4, 26.1, 768 22.4, 25.7, 1024 32.6, 41.2.
-    const bool split = slots_of(a, 16) * ((a.I + 15) / 16) <= 512;
-    // entries of an expert on average: 16 of them are worked on at once, or 32
-    const bool wide = !split && a.T * a.K > 8 * (int64_t)a.E;
-    if (a.out_f32) return wide ? launch_all<MX, 3, 2>(a, split, s) : launch_all<MX, 3, 1>(a, split, s);
-    return wide ? launch_all<MX, 2, 2>(a, split, s) : launch_all<MX, 2, 1>(a, split, s);
 }
 
 }  // namespace

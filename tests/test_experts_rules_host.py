@@ -87,13 +87,22 @@ def test_lists_in_order_are_kept(lists, N, E):
 RULES = r"""
 #include <cstdio>
 #include "experts_rules.hpp"
-int main() {   // "p rows E N"
+static void show(moe::StreamForm f) { std::printf(" %d %d %d %d %d", f.width, f.stage, f.waves, f.split, f.pack); }
+int main() {   // "p rows E N" or "d T H I E K mx parts"
     char what;
     while (std::scanf(" %c", &what) == 1) {
-        long a, b;
-        int d;
-        if (std::scanf("%ld %d %ld", &a, &d, &b) != 3) return 1;
-        std::printf("%d\n", moe::ProductSize{a, b, d}.tile_rows());
+        long a, b, c;
+        int d, e, mx, parts;
+        if (what == 'p') {
+            if (std::scanf("%ld %d %ld", &a, &d, &b) != 3) return 1;
+            std::printf("%d", moe::ProductSize{a, b, d}.tile_rows());
+        } else {
+            if (std::scanf("%ld %ld %ld %d %d %d %d", &a, &b, &c, &e, &d, &mx, &parts) != 7) return 1;
+            const moe::DecodeSize s{a, b, c, d, e, mx != 0, parts};
+            show(s.up());
+            show(s.down());
+        }
+        std::puts("");
     }
 }
 """
@@ -105,6 +114,36 @@ def rules(tmp_path_factory):
     return lambda lines: [[int(v) for v in l.split()] for l in run("\n".join(lines)).splitlines()]
 
 
+def _decode_forms(rules, sizes, mx, parts):
+    got = rules(["d %d %d %d %d %d" % s + f" {int(mx)} {parts}" for s in sizes])
+    as_form = lambda v: (v[0], v[1], v[2], bool(v[3]), bool(v[4]))
+    return [(as_form(g[:5]), as_form(g[5:])) for g in got]
+
+
 def test_tested_products_reach_their_tiles(rules):
     for height, sizes in F.PRODUCT.items():
         assert rules(["p %d %d %d" % s for s in sizes]) == [[height]] * len(sizes), height
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_tested_decode_steps_reach_their_kernels(rules, mx):
+    table = F.MXFP4 if mx else F.BF16
+    assert _decode_forms(rules, table, mx, 2) == list(table.values())
+    wider = [(up, (5,) + down[1:] if down[4] else down) for up, down in table.values()]
+    assert _decode_forms(rules, table, mx, 3) == wider
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_no_form_is_out_of_the_tests(rules, mx):
+    """Every form that a size can have is that of a tested one."""
+    rng = random.Random(mx)
+    step = 32 if mx else 8
+    log = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))
+    sizes = []
+    for _ in range(6000):
+        K = rng.randint(1, 16)
+        sizes.append((log(1, 1024 // K), step * log(1, 16384 // step), step * log(1, 16384 // step), log(1, 1024), K))
+    table = F.MXFP4 if mx else F.BF16
+    seen = _decode_forms(rules, sizes, mx, 2)
+    assert {u for u, _ in seen} == {u for u, _ in table.values()}
+    assert {d for _, d in seen} == {d for _, d in table.values()}

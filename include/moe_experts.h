@@ -72,7 +72,8 @@ int moe_expert_product_mxfp4(const void* a, const void* a_scales, int64_t rows, 
  * outside its limits).  It does not shrink when T, K, H or I grows, so one for the largest
  * sizes serves all; it needs no initialisation and may be reused by consecutive calls on
  * one stream, also from a captured graph.
- * Calls that may run at the same time need workspaces of their own. */
+ * Calls that may run at the same time, or that several host threads enqueue at the same time,
+ * need workspaces of their own. */
 size_t moe_experts_decode_workspace_size(int64_t T, int K, int64_t H, int64_t I);
 
 /* The whole experts' step of a few tokens (T*K <= 1024; H, I <= 2^20), from token rows to
@@ -80,8 +81,8 @@ size_t moe_experts_decode_workspace_size(int64_t T, int K, int64_t H, int64_t I)
  *   out[t] = sum over k of w[t,k] * W2[e] h,  h = silu(W1[e] x[t]) * (W3[e] x[t]),  e = idx[t,k]
  * The sum over k ascends, in f32; entries whose idx is outside [0,E) are skipped whatever
  * their w holds, and a token without any other gets zeros.  h is held between the
- * products with at least 16 bits of significand (24 for an f32 result), over the whole range
- * of f32.
+ * products with at least 16 bits of significand (24 for an f32 result), small ones to within
+ * 2^-134, and finite if it is finite in f32.
  *   x       [T,H] MOE_BF16
  *   idx     int32 [T,K]; w f32 [T,K]
  *   w13     [E,2I,H], I rows of W1 and then I of W3 per expert: wt_dt MOE_BF16

@@ -171,3 +171,45 @@ def test_nan_scales(height):
     mine = rows // E * E
     assert torch.equal(torch.isnan(y[:mine]), want[:mine])
     assert torch.equal(torch.isnan(z[:mine]), want_up[:mine])
+
+
+@pytest.mark.parametrize("E", [256, 257, 300, 513, 1024])
+@pytest.mark.parametrize("rows,N", [(700, 48), (1500, 1072)])
+def test_many_experts(E, rows, N):
+    """More experts than are looked at together, most of them without a row, the last with some."""
+    note(f"many experts E={E} rows={rows} N={N}")
+    rng = np.random.default_rng(E)
+    cnt = np.zeros(E, dtype=np.int32)
+    for e in [0, E - 1, 255] + rng.integers(0, E, 40).tolist():
+        cnt[e] = min(int(rng.integers(1, 40)), rows - 5 - int(cnt.sum()) + int(cnt[e]))
+    cnt = torch.from_numpy(cnt)
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    off[1:] = torch.cumsum(cnt, 0)
+    off += 3
+    g = torch.Generator(device=DEV)
+    g.manual_seed(E)
+    a, w = _random(g, (rows, 160)), _random(g, (E, N, 160))
+    for swiglu in (False, True):
+        y = torch.full((rows, N // 2 if swiglu else N), 7.0, dtype=F32, device=DEV)
+        moe.expert_product_mxfp4(*a, *w, cnt.to(DEV), off.to(DEV), swiglu=swiglu, y=y)
+        torch.cuda.synchronize()
+        _check(y, a, w, cnt, off, swiglu, "experts")
+
+
+def test_longest_rows():
+    """H = 2^24, with scales of 1: every sum is a multiple of 1/4 below 2^22, and exact."""
+    rows, E, N, H = 5, 2, 16, 1 << 24
+    note("longest rows of the product")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(24)
+    a, w = _random(g, (rows, H)), _random(g, (E, N, H))
+    a[1].fill_(127)
+    w[1].fill_(127)
+    cnt, off = torch.tensor([2, 3], dtype=torch.int32), torch.tensor([0, 2, 5], dtype=torch.int32)
+    y = moe.expert_product_mxfp4(*a, *w, cnt.to(DEV), off.to(DEV), out_dtype=F32)
+    torch.cuda.synchronize()
+    va = _values(*a)
+    for e in range(E):
+        z = va[off[e]:off[e + 1]] @ _values(w[0][e], w[1][e]).t()
+        assert z.abs().max() < 2.0 ** 20          # and so are the sums on the way, of random signs
+        assert torch.equal(y[off[e]:off[e + 1]].double(), z)

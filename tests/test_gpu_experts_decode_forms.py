@@ -103,3 +103,17 @@ def test_bits_do_not_change(mx, size):
     for _ in range(2):
         assert torch.equal(first, moe.experts_decode(x, idx, w, w13[0], w2[0], w13[1], w2[1], out_dtype=F32))
         assert torch.equal(first, moe.experts_decode(x, idx, w, a, b, w13[1], w2[1], out_dtype=F32))
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T,H,I,E,K", [(1, 1 << 20, 32, 2, 2), (1, 32, 1 << 20, 2, 2), (1024, 1 << 20, 32, 3, 1),
+                                       (1024, 32, 1 << 20, 3, 1), (64, 1 << 20, 64, 40, 1)])
+def test_largest_sizes(T, H, I, E, K, mx):
+    """Rows of 2^20 elements, x and the parts of h of 2 GiB."""
+    note(f"decode largest T={T} H={H} I={I} mx={mx}")
+    args = _inputs(T, H, I, E, K, mx, False, T + H)
+    x, idx, w, w13, w2 = args
+    y = moe.experts_decode(x, idx, w, w13[0], w2[0], w13[1], w2[1], out_dtype=F32)
+    torch.cuda.synchronize()
+    _check(y, *args, 3)
+    torch.cuda.empty_cache()

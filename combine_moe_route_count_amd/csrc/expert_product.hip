@@ -55,9 +55,6 @@ constexpr int kGroup = 4;         // stages in LDS, and stages whose scales are 
 constexpr int kGroupChunks = kGroup * kStageChunks;
 constexpr int kFp4 = 4;           // the matrix instruction's format code of e2m1
 
-// Ored to an offset below 2^31 it leaves every descriptor's range (2^31 at the most).
-__device__ __forceinline__ uint32_t outside_if(bool b) { return (uint32_t)b << 31; }
-
 constexpr int kRowGroup = 4;       // row tiles of an expert that are worked on side by side
 
 using Lds = __attribute__((address_space(3))) uint8_t;
@@ -159,12 +156,6 @@ __device__ __forceinline__ Tile find_tile(const ProductArgs& a, int64_t b, int c
     t.row0 = (int64_t)first + (int64_t)skip * BM;
     t.rows = cnt - skip * BM < BM ? cnt - skip * BM : BM;
     return t;
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const uint8_t* base, int64_t row,
-                                                          int64_t rows, int64_t row_bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc((void*)(base + row * row_bytes), 0,
-                                             (int)(uint32_t)(rows * row_bytes), kRsrcWord3);
 }
 
 // 16 rows of a stage into LDS, lane l's 16 bytes to l * 16.
@@ -416,27 +407,14 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
     }                                                                                       \
     __builtin_amdgcn_sched_barrier(0)
 
-    // All but the last `flying` loads of every wave have landed, and every wave's LDS reads
-    // are in registers.  The empty asm keeps the compiler from moving memory accesses over
-    // the barrier.
-    auto sync = [](auto flying) {
-        constexpr int N = decltype(flying)::value;
-        static_assert(N < 64, "vmcnt");
-        asm volatile("" ::: "memory");
-        // simm16 of s_waitcnt: vmcnt in bits 3:0 and 15:14, expcnt 6:4 (none), lgkmcnt 11:8 (0)
-        __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x70);
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-    };
     constexpr int kLoads = kLoadsA + kLoadsW;    // of a wave for a stage
 // Stage s, number I of its group, in LDS buffer LDS, its first fragments already read; the
-// next stage is in NEXT, or on its way.
+// next stage is in NEXT, or on its way (s + 2 and s + 3 may be in flight when s + 1 has to be there).
 #define MOE_MX_STAGE(LDS, NEXT, I) \
     stage_scales(I);               \
     read_frags(1, LDS);            \
     MOE_MX_STEP(0);                \
-    sync(two_stages);              \
+    stage_sync<2 * kLoads>();      \
     load_stage(LDS, s + kGroup);   \
     read_frags(0, NEXT);           \
     MOE_MX_STEP(1);                \
@@ -456,10 +434,8 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
     load_stage(lds1, 1);      // past the last stage: zeros
     load_stage(lds2, 2);
     load_stage(lds3, 3);
-    // stages s + 2 and s + 3 may be in flight when s + 1 has to be there
-    constexpr std::integral_constant<int, 2 * kLoads> two_stages{};
     int s = 0;
-    sync(std::integral_constant<int, 3 * kLoads>{});
+    stage_sync<3 * kLoads>();
     read_frags(0, lds0);
     for (int p = 0; p < pairs;) {      // what is loaded behind the last pair is not used
 #pragma unroll
@@ -499,7 +475,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs& a, const Tile& t
 #undef MOE_MX_STEP
     // No load into LDS may be in flight when it is written below, or goes to the next
     // workgroup.
-    sync(std::integral_constant<int, 0>{});
+    stage_sync<0>();
 
     // A lane holds column r of a tile (a row of y) and weight rows 8 * p + 4 * g + 0..3 of it:
     // stores of its own values would be 8 bytes to a row.  Each wave turns 32 rows at a time

@@ -249,15 +249,6 @@ __device__ __forceinline__ u32x4 widen8(uint32_t d, float scale) {
     return u32x4{widen2<0>(d, scale), widen2<1>(d, scale), widen2<2>(d, scale), widen2<3>(d, scale)};
 }
 
-// Ored to an offset below 2^31 it leaves every descriptor's range (2^31 at the most).
-__device__ __forceinline__ uint32_t outside_if(bool b) { return (uint32_t)b << 31; }
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* base, int64_t row,
-                                                          int64_t rows, int64_t row_bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc((char*)base + row * row_bytes, 0,
-                                             (int)(uint32_t)(rows * row_bytes), kRsrcWord3);
-}
-
 // 64 x 16 bytes into LDS.  ONCE: the line is not wanted again (nt).
 template <bool ONCE>
 __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t off) {
@@ -638,21 +629,6 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
         clear();
     };
 
-    // All but the last `flying` loads of every wave have landed, and every wave's LDS reads
-    // are in registers.  The empty asm keeps the compiler from moving memory accesses over
-    // the barrier.
-    auto sync = [](auto flying) {
-        constexpr int F = decltype(flying)::value;
-        static_assert(F < 64, "vmcnt");
-        asm volatile("" ::: "memory");
-        // simm16 of s_waitcnt: vmcnt in bits 3:0 and 15:14, expcnt 6:4 (none), lgkmcnt 11:8 (0)
-        __builtin_amdgcn_s_waitcnt((F & 15) | (F >> 4) << 14 | 0x70);
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    constexpr std::integral_constant<int, 2 * S::kLoads> two_stages{};
-
     int item = blockIdx.x;
     if (item >= items) return;
     __syncthreads();      // the lists are done with their scratch
@@ -685,16 +661,16 @@ void stream_kernel(DecodeArgs a, uint32_t* lists, int down_width, uint16_t* h, i
                                                    r + 16 * (group % kPerLoad * (S::kWords / 4) + j / 4));
             if (more && next_group % kPerLoad == 0) load_scales(next, next_group);
         }
-        sync(two_stages);
+        stage_sync<2 * S::kLoads>();      // two stages may be in flight
         load_stage(lds3, now, group * kGroup + 3);
         use_stage(lds0, 0);
-        sync(two_stages);
+        stage_sync<2 * S::kLoads>();
         load_stage(lds0, next, next_group * kGroup + beyond);
         use_stage(lds1, 1);
-        sync(two_stages);
+        stage_sync<2 * S::kLoads>();
         load_stage(lds1, next, next_group * kGroup + 1 + beyond);
         use_stage(lds2, 2);
-        sync(two_stages);
+        stage_sync<2 * S::kLoads>();
         load_stage(lds2, next, next_group * kGroup + 2 + beyond);
         use_stage(lds3, 3);
         if (last) store_item(item);

@@ -6,6 +6,29 @@
 
 namespace moe {
 
+// Ored to an offset below 2^31 it leaves every descriptor's range (2^31 at the most).
+__device__ __forceinline__ uint32_t outside_if(bool b) { return (uint32_t)b << 31; }
+
+// A buffer of `rows` rows from `row` on: loads from behind the last one give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* base, int64_t row, int64_t rows,
+                                                          int64_t row_bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((char*)base + row * row_bytes, 0,
+                                             (int)(uint32_t)(rows * row_bytes), kRsrcWord3);
+}
+
+// All but the last FLYING loads of every wave have landed, and every wave's LDS reads are in
+// registers.  The empty asm keeps the compiler from moving memory accesses over the barrier.
+template <int FLYING>
+__device__ __forceinline__ void stage_sync() {
+    static_assert(FLYING < 64, "vmcnt");
+    asm volatile("" ::: "memory");
+    // simm16 of s_waitcnt: vmcnt in bits 3:0 and 15:14, expcnt 6:4 (none), lgkmcnt 11:8 (0)
+    __builtin_amdgcn_s_waitcnt((FLYING & 15) | (FLYING >> 4) << 14 | 0x70);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 struct Act {
     float s, c;   // sigmoid and 1 - sigmoid
 };

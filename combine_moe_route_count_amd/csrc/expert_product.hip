@@ -24,11 +24,13 @@
 // Scales are loaded for eight stages at once, 16 bytes by each of two lanes, wherever rows start:
 // loads of single words kept the address unit busier than the matrix cores.
 //
-// Measured on random codes: 2.9 to 3.1e15 operations a second (32768 rows x 4096 x 7168 over
-// 64 experts, SwiGLU), 3.6 to 3.9e15 (8192 x 8192 x 8192), where the matrix instruction alone runs at
-// 6.3e15; all-zero codes take a quarter less time, so it is power that bounds it, and rows of
-// zeros in a tile cost little.  5.9 TB/s of weights where experts have two rows each (128
-// experts, 4096 x 4096).
+// Measured on random codes: 3.0 to 3.1e15 operations a second (32768 rows x 4096 x 7168 over
+// 64 experts, SwiGLU), 3.7 to 3.9e15 (8192 x 8192 x 8192), where the matrix instruction alone runs at
+// 6.3e15.  All-zero codes take a quarter less time: that much of it is power, and rows of zeros in a
+// tile cost little.  The rest is what a tile does beside its matrix instructions: with 128 or 256 rows
+// a CU has one workgroup, so finding the tile, its first loads and its epilogue are covered by nothing
+// (at K = 2048, 32768 rows x 7168, 2.2e15; there the 256-row form without SwiGLU also spills
+// 16 registers).  6.0 TB/s of weights where experts have two rows each (128 experts, 4096 x 4096).
 //
 // Rows behind a segment, weight rows behind N and chunks behind H are loaded as zeros
 // by the range check of the buffer descriptors (their scales too, so a NaN scale of a

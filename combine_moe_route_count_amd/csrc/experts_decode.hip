@@ -22,14 +22,16 @@
 // each, and their sums are added in LDS.
 //
 // h between the products is held in as many bf16 parts as the result can show: 2 (16 bits
-// of significand) for a bf16 result, 3 (24 bits) for an f32 one.  Each part costs one
-// matrix instruction per weight fragment, which bf16 weights have to spare.  MXFP4 weights
+// of significand) for a bf16 result, 3 (24 bits) for an f32 one.  With a third
+// part one bf16 result in some hundreds would be its neighbour, and the relative error against 64
+// bits is 0.0017 with either; it costs 53 -> 63 us (one token, bf16), 293 -> 315 (128 tokens, MXFP4).
+// Each part is one matrix instruction per weight fragment and LDS for its rows.  MXFP4 weights
 // must be widened too and leave less room: where experts have few entries the parts are
 // columns of one instruction, and the columns of an entry are added at the end.
 //
 // Measured, bytes of the weights in use over the time: one token and bf16 weights of 8
 // experts, 1024 x 6144, 54 us, 5.6 TB/s; 32 tokens and MXFP4 weights of 111 experts, 1024 x
-// 7168, 226 us, 5.8 TB/s; bf16, 1024 x 4096, 481 us, 5.8 TB/s.
+// 7168, 225 to 237 us, 5.5 to 5.8 TB/s; bf16, 1024 x 4096, 476 to 481 us, 5.8 TB/s.
 #include <type_traits>
 
 #include "train_device.hpp"

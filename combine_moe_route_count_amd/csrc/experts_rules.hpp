@@ -43,8 +43,10 @@ constexpr int kTileCols = 256;                       // weight rows of a tile of
 //
 // Tile heights 64, 128, 256 by the mean rows of an expert, in us (32 experts with uneven
 // loads, 4096 x 4096): mean 24 62, 64, 72; 64 73, 75, 82; 96 91, 90, 94; 192 135, 117, 122;
-// 256 163, 148, 128; 384 224, 200, 185.  (The mean is that of the buffer's rows: the host does not
-// know the counts.  Padded segments that are mostly empty get higher tiles than their rows need.)
+// 256 163, 148, 128; 384 224, 200, 185.  The mean is that of the buffer's rows, for the host does not
+// know the counts: padded segments that are mostly empty get higher tiles than their rows need.  64
+// experts with room for 256 rows (4096 x 7168, SwiGLU), tiles of 256 and 64: 12 rows in each 228
+// and 188 us, 64 244, 204; 128 271, 287; 200 306, 451.
 // A height whose tiles would leave 100 CUs without one gives way to the next lower, in us:
 // 120 tiles of 256 rows 22.2 against 16.9 with 128, 136 35.7 and 28.4, 168 23.6 and 27.6,
 // 184 37.3 and 44.9; 138 tiles of 128 rows 22.5 against 20.2 with 64, 144 22.8 and 20.8,

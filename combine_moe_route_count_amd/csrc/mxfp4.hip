@@ -9,9 +9,9 @@
 //
 // Rows have no gaps and blocks do not cross rows, so both kernels run over one flat
 // array, one pass, HBM bound.  Quantizing, a lane holds 8 elements (4 lanes a block) and
-// kUnits such units: 32768 x 7168 f32 take 194 us, 5.5 TB/s.  Dequantizing, it makes 16
+// kUnits such units: 32768 x 7168 f32 take 193 us, 5.5 TB/s.  Dequantizing, it makes 16
 // bytes at a time: with 32 (8 f32 elements, two stores to a lane, each half of every line
-// past the caches) the same rows took 364 us, now 171, 6.2 TB/s.
+// past the caches) the same rows took 364 us, now 158 to 170, 6.3 to 6.7 TB/s.
 #include <type_traits>
 
 #include "train_device.hpp"

@@ -13,8 +13,8 @@
 //
 // Both kernels are one pass over the rows, 8 elements of g and the same of u per lane (4
 // where the output is f32, so that a store is 16 bytes a lane and a wave's whole lines),
-// HBM bound: 65536 x 2 x 2048 bf16 with the checkpoint 168 us, 6.4 TB/s; the gradient of the
-// same from the checkpoint, with h, 240 us, 5.0 TB/s; 16384 x 2 x 2048 f32 gradient 139 us.
+// HBM bound: 65536 x 2 x 2048 bf16 with the checkpoint 167 us, 6.5 TB/s; the gradient of the
+// same from the checkpoint, with h, 242 us, 4.9 TB/s; 16384 x 2 x 2048 f32 gradient 139 us.
 // With 8 f32 elements a lane (two stores to a lane, each half of every line) that one took
 // 157.  A workgroup is a power of two of lanes along a row times rows of it, so short rows
 // share one; rows outside every segment are neither read nor written.

@@ -88,7 +88,7 @@ size_t moe_experts_decode_workspace_size(int64_t T, int K, int64_t H, int64_t I)
  *   w13     [E,2I,H], I rows of W1 and then I of W3 per expert: wt_dt MOE_BF16
  *           (H % 8 == 0, I % 8 == 0), or MOE_FP4_E2M1: MXFP4 codes with w13_scales
  *           [E,2I,H/32] (H % 32 == 0, I % 32 == 0); a value past bf16's largest is
- *           infinite
+ *           infinite (infinite weights give infinities as in the formula, 0 times one NaN)
  *   w2      [E,H,I], likewise, with w2_scales [E,H,I/32]; both scales NULL for bf16
  *   out     out [T,H] out_dt (MOE_BF16 or MOE_F32)
  *   ws      at least moe_experts_decode_workspace_size(T, K, H, I) bytes, 256-byte aligned */
@@ -97,8 +97,8 @@ int moe_experts_decode(const void* x, int64_t T, int64_t H, const int32_t* idx, 
                        const void* w2, const void* w2_scales, moe_dtype wt_dt, void* out,
                        moe_dtype out_dt, void* ws, size_t ws_bytes, void* stream);
 
-/* SwiGLU of packed rows, h[r,i] = silu(gu[r,i]) * gu[r,I+i], silu(g) = g / (1 + exp(-g)),
- * and on request the 8-bit checkpoint of gu that moe_swiglu_backward takes.
+/* SwiGLU of packed rows, h[r,i] = silu(gu[r,i]) * gu[r,I+i], silu(g) = g / (1 + exp(-g))
+ * (here and in the products an exp(-|g|) below 2^-126 counts as 0), and on request the 8-bit checkpoint of gu that moe_swiglu_backward takes.
  *   gu      [rows,2I] gu_dt (MOE_BF16 or MOE_F32), I % 8 == 0
  *   packed_cnt, packed_off  the segments (E experts), or both NULL: every row
  *   h       out [rows,I] h_dt (MOE_BF16 or MOE_F32)

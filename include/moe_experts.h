@@ -98,7 +98,8 @@ int moe_experts_decode(const void* x, int64_t T, int64_t H, const int32_t* idx, 
                        moe_dtype out_dt, void* ws, size_t ws_bytes, void* stream);
 
 /* SwiGLU of packed rows, h[r,i] = silu(gu[r,i]) * gu[r,I+i], silu(g) = g / (1 + exp(-g))
- * (here and in the products an exp(-|g|) below 2^-126 counts as 0), and on request the 8-bit checkpoint of gu that moe_swiglu_backward takes.
+ * (here and in the products an exp(-|g|) below 2^-126 counts as 0), and on request the
+ * 8-bit checkpoint of gu that moe_swiglu_backward takes.
  *   gu      [rows,2I] gu_dt (MOE_BF16 or MOE_F32), I % 8 == 0
  *   packed_cnt, packed_off  the segments (E experts), or both NULL: every row
  *   h       out [rows,I] h_dt (MOE_BF16 or MOE_F32)

@@ -553,7 +553,7 @@ __global__ __launch_bounds__(kThreads, (BM <= 64 ? 2 : 1)) void product_kernel(P
 // Few rows and few weight rows: tiles of 32 by 64, so that there are enough of them, and K
 // is split over the waves of a workgroup.  A wave streams its quarter through LDS buffers
 // of its own (stages of 128 elements, four deep), with no barrier until the four sums are
-// joined, in the order of the waves.  One row by 8192 x 8192 takes 14.2 us, 2.5 TB/s: the
+// joined, in the order of the waves.  One row by 8192 x 8192 takes 14.6 us, 2.4 TB/s: the
 // latency of 16 stages a wave and the launch (21.5 with tiles of 64 rows by 256).
 // ---------------------------------------------------------------------------
 template <bool SWIGLU, bool WORDS>
